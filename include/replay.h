@@ -85,6 +85,9 @@ typedef enum {
 #define REPLAY_DEV_ROLLBACK 4     /* n_keep outside [0, n_pos]; that sequence kept none */
 #define REPLAY_DEV_SNAPSHOT 8     /* replay_import: a snapshot or sequence id did not match
                                      the layer; that snapshot was skipped */
+#define REPLAY_DEV_SEQS 16    /* packed sequences: a row id past the batch or named twice (that
+                                 sequence was skipped; the first of equal ids is served), or
+                                 bounds out of order or outside the tokens (skipped) */
 
 typedef struct {
   int32_t batch;   /* B >= 1 */
@@ -343,6 +346,111 @@ int replay_quantize_rows_e4m3(const float* x, int64_t rows, int32_t n, uint8_t* 
 int replay_verify_static_scratch(replay_ctx* ctx, int32_t n_pos, const void* q, const void* k,
                                  const void* v, const float* dt, const float* a, float* y,
                                  uint8_t* flushed, replay_stream_t stream);
+
+/* ---- Around the decode step: a layer's inputs, the scan of prompts, the gated norm ----
+ * What a layer computes before and after the recurrence, and what a prompt goes through
+ * before its first decode step. cfg supplies heads, groups, P, N and io, and, where a call
+ * has a state, batch = the rows of that state (L, max_pos and ckpt are ignored).
+ *
+ * Packed sequences. Prompts are packed one behind the other: sequence s of n_seqs holds
+ * tokens [cu_seqlens[s], cu_seqlens[s + 1]) of `tokens` (device int32 [n_seqs + 1], not
+ * decreasing; lengths of zero are allowed; tokens outside every sequence are neither read
+ * nor written). Sequence s owns row seqs[s] of the state (device int32 [n_seqs], distinct;
+ * NULL = row s, n_seqs <= batch). A negative id is padding: that sequence is skipped, its
+ * outputs are left as they were. resume[s] != 0 (device uint8 [n_seqs]; NULL = none)
+ * continues sequence s from its row; else it starts from zero. Rows that no sequence owns
+ * are left as they were. `status` (device int32 [1], may be NULL) receives
+ * REPLAY_DEV_SEQS. No call allocates device memory or synchronises; each can be captured
+ * into a CUDA graph (once one call of the same kind has run outside the capture), and
+ * replayed on new contents of the same buffers, cu_seqlens, seqs and resume among them.
+ *
+ * Row strides ldx, ldr, ldz are in elements, so that the caller may pass slices of its
+ * projection's rows; x and z rows start on 16-byte boundaries. */
+
+/* The inputs of packed prompts from the projection's rows. x holds D = H*P + 2*G*N
+ * channels a row, v (H*P), then k (G*N), then q (G*N). Per channel and token, within the
+ * sequence,
+ *   c_t = bias + sum_{i < width} w[i] x[t - (width - 1) + i],   out = c_t sigmoid(c_t),
+ * where the rows before the first token are the state's (resume) or zero. Per head
+ *   Delta = softplus(raw + dt_bias),   a = exp(-Delta A).
+ * The state's row becomes the last width - 1 rows of x (with the old rows before them
+ * where the sequence is shorter).
+ *   x:    device [tokens] rows of D io, ldx apart     raw: [tokens] rows of H io, ldr apart
+ *   w:    device [width][D] FP32, width 2..4 (w[width - 1] takes the token itself)
+ *   bias: [D] FP32 or NULL   dt_bias: [H] FP32 or NULL   A: [H] FP32
+ *   conv: device [batch][width - 1][D] io, oldest row first (updated)
+ *   q, k: device [tokens][G][N] io   v: [tokens][H][P] io   dt, a: [tokens][H] FP32 (written)
+ * No output may overlap x, raw or conv. */
+int replay_prompt_inputs(const replay_config* cfg, int32_t width, int64_t tokens, const void* x, int64_t ldx,
+                         const void* raw, int64_t ldr, const float* w, const float* bias, const float* dt_bias,
+                         const float* A, const int32_t* cu_seqlens, const int32_t* seqs, const uint8_t* resume,
+                         int32_t n_seqs, void* conv, void* q, void* k, void* v, float* dt, float* a,
+                         int32_t* status, replay_stream_t stream);
+
+/* The same for one token of each of n rows (decode), from and to the state: row i of x
+ * belongs to state row seqs[i] (NULL = i, n <= batch; a negative id is padding).
+ *   x: device [n] rows of D io   raw: [n] rows of H io   conv: [batch][width - 1][D] (updated)
+ *   q, k: device [n][G][N] io   v: [n][H][P] io   dt, a: [n][H] FP32 (written) */
+int replay_token_inputs(const replay_config* cfg, int32_t width, int32_t n, const void* x, int64_t ldx,
+                        const void* raw, int64_t ldr, const float* w, const float* bias, const float* dt_bias,
+                        const float* A, const int32_t* seqs, void* conv, void* q, void* k, void* v, float* dt,
+                        float* a, int32_t* status, replay_stream_t stream);
+
+/* replay_token_inputs for every sequence of a decode layer, its entries written straight
+ * into the ring (see replay_append_slots): k, v, Delta and a of row b go to the record of
+ * sequence b's next entry, and only q is returned for replay_step_resident, which must be
+ * the next call that changes the buffers.
+ *   x: device [B] rows of D io   conv: [B][width - 1][D] io   q: device [B][G][N] io
+ *   v: device [B][H][P] io, a copy of v for the caller, or NULL
+ * Returns REPLAY_EPENDING while a verify awaits its rollback. */
+int replay_append_inputs(replay_ctx* ctx, int32_t width, const void* x, int64_t ldx, const void* raw, int64_t ldr,
+                         const float* w, const float* bias, const float* dt_bias, const float* A, void* conv,
+                         void* q, void* v, replay_stream_t stream);
+
+/* Scratch bytes that replay_prompt_scan needs for these sizes (0 if none; a multiple of
+ * 256). max_len: an upper estimate of the longest sequence, 0 = unknown; it steers how the
+ * work is split, never the result's meaning. Negative replay_status on bad arguments. */
+int64_t replay_prompt_scan_scratch(const replay_config* cfg, int64_t tokens, int32_t n_seqs, int64_t max_len);
+
+/* The selective scan of packed prompts: per sequence and head, token by token,
+ *   S <- a_t S + Delta_t v_t k_t^T,   y_t = S q_t   (head h uses k and q of group h / (H/G)),
+ * from row seqs[s] of S (resume) or zero, whose final state is written back there.
+ *   q, k: device [tokens][G][N] io   v: [tokens][H][P] io   dt, a: [tokens][H] FP32
+ *   S: device [batch][H][P][N] FP32 (updated)   y: device [tokens][H][P] io (written)
+ *   scratch: device, replay_prompt_scan_scratch bytes, 256-byte aligned (NULL if 0); its
+ *   contents need not survive between calls, but calls that overlap need their own.
+ * No output may overlap an input. */
+int replay_prompt_scan(const replay_config* cfg, int64_t tokens, const void* q, const void* k, const void* v,
+                       const float* dt, const float* a, const int32_t* cu_seqlens, const int32_t* seqs,
+                       const uint8_t* resume, int32_t n_seqs, int64_t max_len, float* S, void* y, void* scratch,
+                       int64_t scratch_bytes, int32_t* status, replay_stream_t stream);
+
+/* Scratch bytes of replay_prefill: replay_prompt_scan_scratch's and one byte a sequence of
+ * the layer, rounded up to a multiple of 256. */
+int64_t replay_prefill_scratch(const replay_ctx* ctx, int64_t tokens, int32_t n_seqs, int64_t max_len);
+
+/* replay_prompt_scan into a decode layer: prompts become the state from which replay_step
+ * decodes on. The rows are the layer's sequences; a resumed sequence's buffered entries are
+ * folded into its checkpoint first. Afterwards the served sequences' buffers are empty,
+ * their checkpoints hold the prompts' final states and a read copy is refreshed; the
+ * others are as they were. Arguments as replay_prompt_scan. Counts as one replay_flush
+ * towards the even number of calls in a captured graph where resume is given, and as no
+ * call where it is NULL. Returns REPLAY_EPENDING while a verify awaits its rollback. */
+int replay_prefill(replay_ctx* ctx, int64_t tokens, const void* q, const void* k, const void* v, const float* dt,
+                   const float* a, const int32_t* cu_seqlens, const int32_t* seqs, const uint8_t* resume,
+                   int32_t n_seqs, int64_t max_len, void* y, void* scratch, int64_t scratch_bytes,
+                   replay_stream_t stream);
+
+/* The gated norm of a layer's outputs. With u = (y + D_h v) z sigmoid(z) per element,
+ *   out = u weight / sqrt(mean(u^2) + eps),
+ * the mean over each of norm_groups equal parts of a row of H*P (a multiple of 8 each).
+ *   y: device [rows][H][P], FP32 or io (y_type: a replay_dtype)   z: [rows] rows of H*P io, ldz apart
+ *   v: device [rows][H][P] io and D: [H] FP32, or both NULL (no skip term)
+ *   weight: device [H*P] FP32   out: device [rows][H*P] io (written; may be z or v, or a y
+ *   of the same type, itself, where that is dense) */
+int replay_gated_norm(const replay_config* cfg, int64_t rows, const void* y, int32_t y_type, const void* z,
+                      int64_t ldz, const void* v, const float* D, const float* weight, int32_t norm_groups,
+                      float eps, void* out, replay_stream_t stream);
 
 /* Static text for a replay_status code. */
 const char* replay_strerror(int code);

@@ -14,6 +14,16 @@ provides device memory and streams.
     r.rollback(n_keep)                         # keep n_keep[b] of them (pointer move)
     r.flush()                                  # fold every buffer into the checkpoint
 
+Around the step, from the rows of a layer's projection (gate | v k q channels | step
+sizes) to the rows of its output projection:
+
+    x, raw, z = proj[:, HP:HP + D], proj[:, HP + D:], proj[:, :HP]
+    q, k, v, dt, a = prompt_inputs(cfg, conv, x, raw, w, A, cu_seqlens)  # prompts, packed
+    y = r.prefill(q, k, v, dt, a, cu_seqlens)  # their outputs; their states into the layer
+    o = gated_norm(cfg, y, z, weight, v=v, D=D_skip)
+    q, v = r.append_inputs(conv, x1, raw1, w, A)  # one token: its entry into the ring
+    o = gated_norm(cfg, r.step_resident(q), z1, weight, v=v, D=D_skip)
+
 Small batches are bound by the host's launch rate; an even number of ``step`` calls on
 fixed input and output tensors can be captured in a CUDA graph once one call has run
 outside the capture (the conditions are in ``include/replay.h``). Each call flips which
@@ -39,6 +49,7 @@ from . import _abi
 from ._abi import (  # noqa: F401
     DEV_POINTER,
     DEV_ROLLBACK,
+    DEV_SEQS,
     DEV_SNAPSHOT,
     DEV_WAIT_TIMEOUT,
     ReplayError,
@@ -49,7 +60,7 @@ from ._abi import (  # noqa: F401
 
 __all__ = ["Config", "Replay", "alloc_buffers", "ring_capacity", "ring_record_bytes", "ring_k_record_bytes",
            "code_shape", "snapshot_bytes", "eager_step", "eager_step_fp8", "quantize_rows_e4m3", "quantize_rows_e2m1",
-           "ReplayError", "load", "strerror"]
+           "prompt_inputs", "token_inputs", "prompt_scan", "gated_norm", "ReplayError", "load", "strerror"]
 
 
 _CKPT = {"f32": _abi.REPLAY_CKPT_F32, "f32_fp8read": _abi.REPLAY_CKPT_F32_FP8READ,
@@ -158,6 +169,85 @@ def _ptr(t, shape=None, dtype=None, name="tensor"):
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _rows(t, n, width, dtype, name):
+    """Pointer and row stride (elements) of a 2-D tensor whose rows may lie apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != width:
+        raise ValueError(f"{name} must have shape {(n, width)}, got {tuple(t.shape)}")
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    # the stride of a single row says nothing
+    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if n > 1 else (width + 7) // 8 * 8
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors are on different devices: {first.device} and {t.device}")
+    return first.device
+
+
+class _On:
+    """Makes `device` current, and `stream` (None: the device's current one) the stream of
+    the allocations inside, so that scratch is not handed to another stream's work early."""
+
+    def __init__(self, device, stream):
+        self._dev = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        self._stream = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self._dev is not None:
+            self._dev.__enter__()
+        if self._stream is not None:
+            self._stream.__enter__()
+        return _stream(None)
+
+    def __exit__(self, *exc):
+        if self._stream is not None:
+            self._stream.__exit__(*exc)
+        if self._dev is not None:
+            self._dev.__exit__(*exc)
+
+
+def _channels(cfg):
+    return cfg.heads * cfg.P + 2 * cfg.groups * cfg.N
+
+
+def _filter_args(cfg, conv, w, A, bias, dt_bias):
+    """width and the pointers w, bias, dt_bias, A, conv of the convolution's arguments."""
+    D, f32 = _channels(cfg), torch.float32
+    if w.dim() != 2:
+        raise ValueError(f"w must have shape (width, {D}), got {tuple(w.shape)}")
+    width = w.shape[0]
+    return (width, _ptr(w, (width, D), f32, "w"), _ptr(bias, (D,), f32, "bias"),
+            _ptr(dt_bias, (cfg.heads,), f32, "dt_bias"), _ptr(A, (cfg.heads,), f32, "A"),
+            _ptr(conv, (cfg.batch, width - 1, D), cfg.io_dtype, "conv"))
+
+
+def _packed_args(cu_seqlens, seqs, resume):
+    """n_seqs and the pointers cu_seqlens, seqs, resume."""
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must be a tensor of n_seqs + 1 offsets")
+    n = cu_seqlens.shape[0] - 1
+    return (n, _ptr(cu_seqlens, (n + 1,), torch.int32, "cu_seqlens"), _ptr(seqs, (n,), torch.int32, "seqs"),
+            _ptr(resume, (n,), torch.uint8, "resume"))
+
+
+def _alloc_inputs(cfg, n, device, out):
+    """q, k, v, dt, a of n tokens: `out` checked, or new tensors."""
+    t, f32 = cfg.io_dtype, torch.float32
+    shapes = (((n, cfg.groups, cfg.N), t), ((n, cfg.groups, cfg.N), t), ((n, cfg.heads, cfg.P), t),
+              ((n, cfg.heads), f32), ((n, cfg.heads), f32))
+    if out is None:
+        out = tuple(torch.empty(s, device=device, dtype=d) for s, d in shapes)
+    return out, [_ptr(o, s, d, name) for o, (s, d), name in zip(out, shapes, ("q", "k", "v", "dt", "a"), strict=True)]
 
 
 class Replay:
@@ -289,6 +379,44 @@ class Replay:
                                       _ptr(src, (n, snapshot_bytes(self.cfg)), torch.uint8, "src"), _stream(stream)),
               "replay_import")
 
+    def append_inputs(self, conv, x, raw, w, A, bias=None, dt_bias=None, q=None, v=None, stream=None):
+        """token_inputs() of every sequence, its entry written straight into the ring; returns
+        q for step_resident(), which must come next, and v (for gated_norm's skip term)."""
+        cfg, t = self.cfg, self.cfg.io_dtype
+        B, H, G, P, N = cfg.batch, cfg.heads, cfg.groups, cfg.P, cfg.N
+        width, *ptrs, cp = _filter_args(cfg, conv, w, A, bias, dt_bias)
+        xp, ldx = _rows(x, B, _channels(cfg), t, "x")
+        rp, ldr = _rows(raw, B, H, t, "raw")
+        with _On(_same_device(self.buffers["S0"], conv, x, raw, w, A, bias, dt_bias, q, v), stream) as st:
+            if q is None:
+                q = torch.empty(B, G, N, device=x.device, dtype=t)
+            if v is None:
+                v = torch.empty(B, H, P, device=x.device, dtype=t)
+            check(self._lib.replay_append_inputs(self._ctx, width, xp, ldx, rp, ldr, *ptrs, cp,
+                                                 _ptr(q, (B, G, N), t, "q"), _ptr(v, (B, H, P), t, "v"), st),
+                  "replay_append_inputs")
+        return q, v
+
+    def prefill(self, q, k, v, dt, a, cu_seqlens, seqs=None, resume=None, y=None, max_len=0, scratch=None, stream=None):
+        """prompt_scan() into the layer: packed prompts become the states that step() decodes
+        on from. Sequence i is the layer's sequence seqs[i]; where resume[i], it continues
+        from that sequence's checkpoint and buffered entries. Returns y [T][H][P] io."""
+        n, cu, sp, rp = _packed_args(cu_seqlens, seqs, resume)
+        T = q.shape[0]
+        ptrs, y_shape = _scan_args(self.cfg, T, q, k, v, dt, a)
+        with _On(_same_device(self.buffers["S0"], q, k, v, dt, a, cu_seqlens, seqs, resume, y, scratch), stream) as st:
+            if y is None:
+                y = torch.empty(y_shape, device=q.device, dtype=self.cfg.io_dtype)
+            need = self._lib.replay_prefill_scratch(self._ctx, T, n, max_len)
+            check(min(need, 0), "replay_prefill_scratch")
+            if scratch is None:
+                scratch = torch.empty(need, device=q.device, dtype=torch.uint8)
+            check(self._lib.replay_prefill(self._ctx, T, *ptrs, cu, sp, rp, n, max_len,
+                                           _ptr(y, y_shape, self.cfg.io_dtype, "y"),
+                                           _ptr(scratch, None, torch.uint8, "scratch"), scratch.numel(), st),
+                  "replay_prefill")
+        return y
+
     def rollback(self, n_keep, stream=None):
         """Keep n_keep[b] (int32 [B] on the device) of the pending verify's positions."""
         check(self._lib.replay_rollback(self._ctx, _ptr(n_keep, (self.cfg.batch,), torch.int32, "n_keep"),
@@ -383,3 +511,101 @@ def quantize_rows_e4m3(x, codes=None, scale=None, stream=None):
                                            _ptr(scale, x.shape[:-1], torch.float32, "scale"), _stream(stream)),
           "replay_quantize_rows_e4m3")
     return codes, scale
+
+
+def prompt_inputs(cfg: Config, conv, x, raw, w, A, cu_seqlens, bias=None, dt_bias=None, seqs=None, resume=None,
+                  out=None, status=None, stream=None):
+    """The inputs of packed prompts from the projection's rows: causal convolution with SiLU
+    of the channels x [T][D] (v | k | q; rows may be slices of wider ones), split, and
+    Delta = softplus(raw + dt_bias), a = exp(-Delta A) of the raw step sizes [T][H]. conv
+    [batch][width - 1][D] (io) holds each row's last raw inputs: read where resume[s],
+    always updated. w [width][D], bias [D], dt_bias, A [H] are FP32; cu_seqlens int32
+    [n + 1], seqs int32 [n] (rows; None = 0..n-1), resume uint8 [n] (None = none).
+    Returns (q, k, v, dt, a)."""
+    width, *ptrs, cp = _filter_args(cfg, conv, w, A, bias, dt_bias)
+    n, cu, sp, rp = _packed_args(cu_seqlens, seqs, resume)
+    T = x.shape[0]
+    xp, ldx = _rows(x, T, _channels(cfg), cfg.io_dtype, "x")
+    rawp, ldr = _rows(raw, T, cfg.heads, cfg.io_dtype, "raw")
+    device = _same_device(x, conv, raw, w, A, cu_seqlens, bias, dt_bias, seqs, resume, status, *(out or ()))
+    with _On(device, stream) as st:
+        out, outs = _alloc_inputs(cfg, T, device, out)
+        check(load().replay_prompt_inputs(ctypes.byref(cfg.c()), width, T, xp, ldx, rawp, ldr, *ptrs, cu, sp, rp, n, cp,
+                                          *outs, _ptr(status, (1,), torch.int32, "status"), st),
+              "replay_prompt_inputs")
+    return out
+
+
+def token_inputs(cfg: Config, conv, x, raw, w, A, bias=None, dt_bias=None, seqs=None, out=None, status=None,
+                 stream=None):
+    """prompt_inputs() for one decode token of each of n rows, from and to the state: row i
+    of x belongs to row seqs[i] of conv (None = i; a negative id is padding)."""
+    width, *ptrs, cp = _filter_args(cfg, conv, w, A, bias, dt_bias)
+    n = x.shape[0]
+    xp, ldx = _rows(x, n, _channels(cfg), cfg.io_dtype, "x")
+    rawp, ldr = _rows(raw, n, cfg.heads, cfg.io_dtype, "raw")
+    device = _same_device(x, conv, raw, w, A, bias, dt_bias, seqs, status, *(out or ()))
+    with _On(device, stream) as st:
+        out, outs = _alloc_inputs(cfg, n, device, out)
+        check(load().replay_token_inputs(ctypes.byref(cfg.c()), width, n, xp, ldx, rawp, ldr, *ptrs,
+                                         _ptr(seqs, (n,), torch.int32, "seqs"), cp, *outs,
+                                         _ptr(status, (1,), torch.int32, "status"), st), "replay_token_inputs")
+    return out
+
+
+def _scan_args(cfg, T, q, k, v, dt, a):
+    """Pointers q, k, v, dt, a of T packed tokens, and the shape of y."""
+    t, f32 = cfg.io_dtype, torch.float32
+    kn, hp = (T, cfg.groups, cfg.N), (T, cfg.heads, cfg.P)
+    return (_ptr(q, kn, t, "q"), _ptr(k, kn, t, "k"), _ptr(v, hp, t, "v"), _ptr(dt, hp[:2], f32, "dt"),
+            _ptr(a, hp[:2], f32, "a")), hp
+
+
+def prompt_scan(cfg: Config, S, q, k, v, dt, a, cu_seqlens, seqs=None, resume=None, y=None, max_len=0, scratch=None,
+                status=None, stream=None):
+    """The selective scan of packed prompts: S <- a S + dt v k^T, y = S q token by token, from
+    row seqs[s] of S [batch][H][P][N] (FP32) where resume[s], else from zero; the final
+    states go back to S. q, k [T][G][N], v [T][H][P] (io), dt, a [T][H] (FP32), cu_seqlens
+    int32 [n + 1], seqs int32 [n], resume uint8 [n]. max_len, if known, steers how the work
+    is split. Returns y [T][H][P] (io)."""
+    n, cu, sp, rp = _packed_args(cu_seqlens, seqs, resume)
+    T = q.shape[0]
+    ptrs, y_shape = _scan_args(cfg, T, q, k, v, dt, a)
+    Sp = _ptr(S, (cfg.batch, cfg.heads, cfg.P, cfg.N), torch.float32, "S")
+    device = _same_device(q, S, k, v, dt, a, cu_seqlens, seqs, resume, y, scratch, status)
+    lib, c = load(), cfg.c()
+    with _On(device, stream) as st:
+        if y is None:
+            y = torch.empty(y_shape, device=device, dtype=cfg.io_dtype)
+        if scratch is None:
+            need = lib.replay_prompt_scan_scratch(ctypes.byref(c), T, n, max_len)
+            check(min(need, 0), "replay_prompt_scan_scratch")
+            if need:
+                scratch = torch.empty(need, device=device, dtype=torch.uint8)
+        check(lib.replay_prompt_scan(ctypes.byref(c), T, *ptrs, cu, sp, rp, n, max_len, Sp,
+                                     _ptr(y, y_shape, cfg.io_dtype, "y"), _ptr(scratch, None, torch.uint8, "scratch"),
+                                     0 if scratch is None else scratch.numel(),
+                                     _ptr(status, (1,), torch.int32, "status"), st), "replay_prompt_scan")
+    return y
+
+
+def gated_norm(cfg: Config, y, z, weight, v=None, D=None, norm_groups=1, eps=1e-5, out=None, stream=None):
+    """The gated norm of a layer's outputs: u = (y + D v) silu(z), out = u weight /
+    sqrt(mean(u^2) + eps), the mean over each of norm_groups equal parts of a row. y
+    [T][H][P] (FP32 or io), z [T][H*P] (io; rows may be slices of wider ones), weight
+    [H*P] FP32; v [T][H][P] (io) and D [H] (FP32) for the skip term. Returns [T][H*P] io."""
+    T, hp, t = y.shape[0], (y.shape[0], cfg.heads, cfg.P), cfg.io_dtype
+    width = cfg.heads * cfg.P
+    y_type = _abi.REPLAY_F32 if y.dtype == torch.float32 else _abi.REPLAY_BF16
+    if y.dtype not in (torch.float32, t):
+        raise ValueError(f"y must have dtype {torch.float32} or {t}, got {y.dtype}")
+    zp, ldz = _rows(z, T, width, t, "z")
+    device = _same_device(y, z, weight, v, D, out)
+    with _On(device, stream) as st:
+        if out is None:
+            out = torch.empty(T, width, device=device, dtype=t)
+        check(load().replay_gated_norm(ctypes.byref(cfg.c()), T, _ptr(y, hp, y.dtype, "y"), y_type, zp, ldz,
+                                       _ptr(v, hp, t, "v"), _ptr(D, (cfg.heads,), torch.float32, "D"),
+                                       _ptr(weight, (width,), torch.float32, "weight"), norm_groups, eps,
+                                       _ptr(out, (T, width), t, "out"), st), "replay_gated_norm")
+    return out

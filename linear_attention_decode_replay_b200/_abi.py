@@ -34,6 +34,7 @@ DEV_WAIT_TIMEOUT = 1
 DEV_POINTER = 2
 DEV_ROLLBACK = 4
 DEV_SNAPSHOT = 8
+DEV_SEQS = 16
 
 
 class ReplayError(RuntimeError):
@@ -91,6 +92,17 @@ def load() -> ctypes.CDLL:
         "eager_step_fp8": (ctypes.c_int, [cfgp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
         "replay_quantize_rows_e4m3": (ctypes.c_int, [vp, i64, i32, vp, vp, vp]),
         "replay_quantize_rows_e2m1": (ctypes.c_int, [vp, i64, i32, vp, vp, vp]),
+        "replay_prompt_inputs": (ctypes.c_int, [cfgp, i32, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, i32, vp,
+                                                vp, vp, vp, vp, vp, vp, vp]),
+        "replay_token_inputs": (ctypes.c_int, [cfgp, i32, i32, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                               vp, vp, vp]),
+        "replay_append_inputs": (ctypes.c_int, [vp, i32, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "replay_prompt_scan_scratch": (i64, [cfgp, i64, i32, i64]),
+        "replay_prompt_scan": (ctypes.c_int, [cfgp, i64, vp, vp, vp, vp, vp, vp, vp, vp, i32, i64, vp, vp, vp, i64, vp,
+                                              vp]),
+        "replay_prefill_scratch": (i64, [vp, i64, i32, i64]),
+        "replay_prefill": (ctypes.c_int, [vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, i32, i64, vp, vp, i64, vp]),
+        "replay_gated_norm": (ctypes.c_int, [cfgp, i64, vp, i32, vp, i64, vp, vp, vp, i32, ctypes.c_float, vp, vp]),
         "replay_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     }
     for name, (res, args) in sig.items():

@@ -1,0 +1,98 @@
+// Device helpers of the operators around the decode step: 16-byte vectors of inputs as
+// floats, the rows that packed sequences own, and programmatic dependent launch.
+#pragma once
+
+#include "layer_params.h"
+#include "replay_device.cuh"
+
+namespace replay {
+
+constexpr int32_t kErrSeqs = 1 << 4;  // a bad or repeated row id, or sequence bounds out of order
+
+// A vector of 16 bytes of inputs: 4 floats or 8 BF16.
+template <typename IO>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int n = 4;
+  __device__ __forceinline__ static void unpack(uint4 u, float* f) {
+    f[0] = __uint_as_float(u.x);
+    f[1] = __uint_as_float(u.y);
+    f[2] = __uint_as_float(u.z);
+    f[3] = __uint_as_float(u.w);
+  }
+  __device__ __forceinline__ static uint4 pack(const float* f) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int n = 8;
+  __device__ __forceinline__ static void unpack(uint4 u, float* f) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // a BF16 is the upper half of the FP32 of the same value
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  __device__ __forceinline__ static uint32_t pack2(float lo, float hi) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&t);
+  }
+  __device__ __forceinline__ static uint4 pack(const float* f) {
+    return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+  }
+};
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// Let the next kernel on the stream be scheduled, and wait until the one before it has
+// completed: nothing in global memory is touched before this returns.
+__device__ __forceinline__ void pdl_enter() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Tokens [begin, end) of sequence s; false (recorded in the status word) where its bounds
+// are out of order or outside the packed tokens.
+__device__ __forceinline__ bool seq_bounds(const Packed& pk, int s, int64_t& begin, int64_t& end) {
+  begin = pk.cu[s];
+  end = pk.cu[s + 1];
+  const bool ok = begin >= 0 && end >= begin && end <= pk.tokens;
+  if (!ok && pk.status) atomicOr(pk.status, kErrSeqs);
+  return ok;
+}
+
+// The state row of sequence s, by a whole warp; -1 for a padding entry (a negative id),
+// and (recorded in the status word) for an id past the batch or one that an earlier
+// sequence has: the first of equal ids is served.
+__device__ __forceinline__ int seq_row(const Packed& pk, int s) {
+  if (!pk.seqs) return s;  // the host checked n_seqs <= batch
+  const int row = pk.seqs[s];
+  if (row < 0) return -1;
+  bool bad = row >= pk.batch;
+  for (int e = threadIdx.x & 31; e < s; e += 32) bad |= pk.seqs[e] == row;
+  bad = __any_sync(0xffffffffu, bad);
+  if (bad && pk.status && (threadIdx.x & 31) == 0) atomicOr(pk.status, kErrSeqs);
+  return bad ? -1 : row;
+}
+
+// Launches `kern` so that its blocks may be scheduled while the previous kernel on the
+// stream drains (pdl_enter waits for it).
+template <typename P>
+cudaError_t pdl_launch(void (*kern)(const P), dim3 grid, int threads, int smem, cudaStream_t s, const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+}  // namespace replay

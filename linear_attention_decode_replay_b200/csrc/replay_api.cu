@@ -10,78 +10,24 @@
 
 #include "../../include/replay.h"
 #include "replay_device.cuh"
+#include "replay_ctx.h"
 #include "replay_launch.h"
 
+using replay::aligned;
+using replay::ckpt_kind;
+using replay::device_info;
+using replay::DeviceInfo;
 using replay::KParams;
+using replay::record_bytes;
+using replay::record_k_bytes;
+using replay::ring_capacity;
+using replay::round_up;
 using replay::SnapParams;
-
-struct replay_ctx {
-  replay_config cfg;
-  replay_buffers bufs;
-  int cap;
-  int parity;   // which half of counts holds the current pointer words
-  int pending;  // n_pos of an unresolved verify, 0 if none
-  int device;
-  int num_sms;
-  KParams kp_step, kp_verify, kp_flush;  // prebuilt launch layouts (pointers filled per call)
-  int verify_ok;                          // kp_verify was built (max_pos > 1)
-  int smem_optin;                         // the device's per-block shared-memory limit
-  KParams kp_static[replay::kMaxPos + 1]; // replay_verify_static_scratch layouts, by n_pos
-  int kp_static_ok[replay::kMaxPos + 1];  // ... built on first use
-};
+using replay::validate_config;
 
 namespace {
 
 constexpr int kHeaderBytes = replay::kHeaderBytes;  // the kernel's mbarriers and flags
-
-inline int round_up(int x, int m) { return (x + m - 1) / m * m; }
-inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-int validate_config(const replay_config* c, bool needs_window) {
-  if (!c) return REPLAY_EINVAL;
-  if (c->batch < 1 || c->heads < 1 || c->groups < 1 || c->heads % c->groups) return REPLAY_EINVAL;
-  if (c->P < 8 || c->P > 256 || c->P % 8) return REPLAY_EINVAL;
-  if (c->N != 16 && c->N != 32 && c->N != 64 && c->N != 128) return REPLAY_EINVAL;
-  if ((int64_t)c->P * c->N * 4 > 65536) return REPLAY_EINVAL;
-  if (c->io != REPLAY_F32 && c->io != REPLAY_BF16) return REPLAY_EINVAL;
-  if ((int64_t)c->batch * c->heads > INT32_MAX / 2) return REPLAY_EINVAL;
-  if (needs_window) {
-    if (c->L < 1 || c->L > replay::kMaxWindow) return REPLAY_EINVAL;
-    if (c->max_pos < 1 || c->max_pos > replay::kMaxPos || c->max_pos > c->L) return REPLAY_EINVAL;
-    if (c->ckpt != REPLAY_CKPT_F32 && c->ckpt != REPLAY_CKPT_F32_FP8READ && c->ckpt != REPLAY_CKPT_F32_FP4READ)
-      return REPLAY_EINVAL;
-  }
-  return REPLAY_OK;
-}
-
-int ring_capacity(const replay_config& c) { return c.L + c.max_pos; }
-// head record: v (P io values), Delta, a; k record: k (N io values)
-int record_bytes(const replay_config& c) {
-  const int s_io = c.io == REPLAY_BF16 ? 2 : 4;
-  return round_up(c.P * s_io + 8, 16);
-}
-// k record: k (N io values), then 16 bytes of padding. The padding staggers consecutive
-// records by four shared-memory banks once a unit's records sit in a stage, so that the
-// lanes that read several entries' k at once (one entry per lane pair or quarter) spread
-// over all 32 banks; without it every record starts on the same bank.
-int record_k_bytes(const replay_config& c) { return c.N * (c.io == REPLAY_BF16 ? 2 : 4) + 16; }
-int ckpt_kind(int ckpt) {
-  return ckpt == REPLAY_CKPT_F32_FP8READ ? replay::kCkptFp8 : ckpt == REPLAY_CKPT_F32_FP4READ ? replay::kCkptFp4
-                                                                                              : replay::kCkptF32;
-}
-
-struct DeviceInfo {
-  int device, num_sms, smem_optin;
-};
-
-int device_info(DeviceInfo* d) {
-  if (cudaGetDevice(&d->device) != cudaSuccess) return REPLAY_ECUDA;
-  if (cudaDeviceGetAttribute(&d->num_sms, cudaDevAttrMultiProcessorCount, d->device) != cudaSuccess)
-    return REPLAY_ECUDA;
-  if (cudaDeviceGetAttribute(&d->smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, d->device) != cudaSuccess)
-    return REPLAY_ECUDA;
-  return REPLAY_OK;
-}
 
 // Shared-memory layout of one launch mode. nq_alloc = query slots per stage, jmax =
 // entries a stage holds (buffer + new), lfold = most entries one unit folds; fp8_eager:

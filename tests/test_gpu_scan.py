@@ -1,0 +1,234 @@
+"""The scan of packed prompts against the float64 oracle.
+
+Bound. Every output is a sum of terms Delta v k q times decays. The scan of the operands'
+magnitudes, M, is the sum of the terms' magnitudes. In FP32 arithmetic a term passes at
+most 2 roundings a token that it decays through (the product and the sum it joins) and
+N + 8 for its own products and the dot product with q, so
+    |error| <= (2 T + N + 8) 2^-24 M
+for T tokens of a sequence. BF16 outputs add half a step of the result. A kernel that
+feeds tensor cores splits an FP32 factor x into BF16 parts with a remainder of at most
+2^-16 |x| (two parts) or 2^-23 |x| (three); outputs that are themselves rounded to BF16
+are given 2^-14 M for their two factors so split."""
+
+import dataclasses
+
+import numpy as np
+import pytest
+import torch
+
+import linear_attention_decode_replay_b200 as lar
+from linear_attention_decode_replay_b200 import _abi
+from layer_harness import HALF, U32, Case, assert_within, f64, packed, scan_inputs
+from oracle import layer_oracle as lo
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
+
+CASES = [
+    Case("one_token", 2, 2, 16, 16, (1,), "f32"),
+    Case("tiny", 2, 2, 16, 16, (37,), "f32"),
+    Case("p8", 3, 1, 8, 16, (5, 130), "bf16"),
+    Case("n32_odd", 6, 2, 24, 32, (7, 0, 129, 1), "bf16", resume="some", rows=6, lead=3, tail=5),
+    Case("n64", 4, 4, 64, 64, (127, 128, 129), "bf16", resume="all"),
+    Case("n64_p256", 2, 1, 256, 64, (70, 200), "bf16", resume="some"),
+    Case("n128_p64", 8, 4, 64, 128, (300, 64, 256), "bf16", resume="some", rows=4),
+    Case("n128_p64_shared", 8, 1, 64, 128, (1000,), "bf16", resume="all"),
+    Case("n128_p80", 5, 5, 80, 128, (255, 2, 257), "bf16", resume="all", tail=200),
+    Case("n128_p128", 4, 2, 128, 128, (640, 3), "bf16"),
+    Case("f32_n128", 4, 2, 64, 128, (200, 0, 77), "f32", resume="some", rows=5, lead=1),
+    Case("f32_p128", 2, 2, 128, 128, (140,), "f32", resume="all"),
+    Case("f32_n64_p40", 2, 1, 40, 64, (33, 131), "f32"),
+    Case("many_short", 4, 2, 64, 128, tuple(1 + i % 5 for i in range(70)), "bf16", resume="some", rows=80),
+    Case("long", 2, 1, 64, 128, (5003,), "bf16", resume="all"),
+    Case("long_f32", 1, 1, 32, 64, (3001, 40), "f32"),
+]
+
+
+def check(case, ins, got_y, got_S, want, mag, cu, seqs, resume):
+    (y, S), (my, mS) = want, mag
+    T = max(max(case.lens), 1)
+    roundings = (2 * T + case.N + 8) * U32
+    by = roundings * my + (HALF["bf16"] * np.abs(y) + 2.0 ** -14 * my if case.io == "bf16" else 0) + 1e-37
+    live = np.zeros(case.T, bool)
+    for _, t0, t1, _ in lo.rows_served(f64(cu), f64(seqs), case.batch):
+        live[t0:t1] = True
+    assert_within(f64(got_y)[live], y[live], by[live], f"{case.name}: y")
+    assert_within(got_S, S, roundings * mS + 1e-37, f"{case.name}: S")
+    return live
+
+
+def run(case, ins, max_len=0, **kw):
+    q, k, v, dt, a, S = ins
+    cu, seqs, resume = packed(case)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    S = S.clone()
+    y = torch.full((case.T, case.H, case.P), 7.0, device="cuda", dtype=case.dtype)
+    out = lar.prompt_scan(case.cfg(), S, q, k, v, dt, a, cu, seqs=seqs, resume=resume, y=y, max_len=max_len,
+                          status=status, **kw)
+    assert out is y and status.item() == 0
+    return y, S, cu, seqs, resume
+
+
+def oracle(ins, cu, seqs, resume):
+    args = [f64(t) for t in ins] + [f64(cu), f64(seqs), f64(resume)]
+    return lo.prompt_scan(*args), lo.prompt_scan_magnitude(*args)
+
+
+@pytest.mark.parametrize("case", CASES, ids=[c.name for c in CASES])
+def test_scan_matches_the_oracle(case):
+    ins = scan_inputs(case)
+    y, S, cu, seqs, resume = run(case, ins)
+    want, mag = oracle(ins, cu, seqs, resume)
+    live = check(case, ins, y, S, want, mag, cu, seqs, resume)
+    assert (y[torch.from_numpy(~live).cuda()] == 7).all()  # tokens outside every sequence
+    y2, S2, *_ = run(case, ins, max_len=max(case.lens))
+    check(case, ins, y2, S2, want, mag, cu, seqs, resume)
+    y3, S3, *_ = run(case, ins)  # bit for bit the same again
+    assert torch.equal(y, y3) and torch.equal(S, S3)
+
+
+@pytest.mark.parametrize("decay", [0.0, 1.0, 0.999, -0.5, 1e-30])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_scan_with_constant_decay(decay, io):
+    """Forgetting everything (a = 0: no logarithm of it may be taken), nothing, and decays of
+    either sign; products that underflow."""
+    case = Case("decay", 2, 1, 64, 128, (300, 20), io, resume="all")
+    ins = scan_inputs(case, decay=decay)
+    ins[3] = ins[3].clone()
+    y, S, cu, seqs, resume = run(case, ins)
+    check(case, ins, y, S, *oracle(ins, cu, seqs, resume), cu, seqs, resume)
+
+
+def test_steps_of_zero_and_mixed_decays():
+    case = Case("mixed", 3, 3, 64, 64, (400,), "bf16", resume="all", seed=4)
+    ins = scan_inputs(case)
+    dt, a = ins[3], ins[4]
+    dt[::7] = 0
+    a[5::50] = 0
+    a[::3] = 1
+    y, S, cu, seqs, resume = run(case, ins)
+    check(case, ins, y, S, *oracle(ins, cu, seqs, resume), cu, seqs, resume)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("what", ["q", "k", "v", "dt", "a"])
+def test_bad_values_reach_only_what_follows_them(io, bad, what):
+    """A NaN or an infinity at one token leaves the tokens before it, the other sequences and
+    the other heads as they were."""
+    case = Case("bad", 2, 2, 64, 128, (150, 200, 130), io, resume="all", seed=2)
+    ins = scan_inputs(case)
+    y0, S0, cu, seqs, resume = run(case, ins)
+    t = 150 + 77  # token 77 of sequence 1, head 0
+    x = [t_.clone() for t_ in ins]
+    x["q k v dt a".split().index(what)][(t, 0, 5) if what in "qkv" else (t, 0)] = bad
+    y1, S1, *_ = run(case, x)
+    same = torch.ones(case.T, case.H, dtype=torch.bool, device="cuda")
+    same[t:350, 0] = False
+    assert torch.equal(y0[same], y1[same])
+    assert torch.equal(S0[[0, 2]], S1[[0, 2]]) and torch.equal(S0[1, 1], S1[1, 1])
+    want, _ = lo.prompt_scan(*[f64(i) for i in x], f64(cu), f64(seqs), f64(resume))
+    got = f64(y1)
+    assert np.array_equal(np.isfinite(got[t:350, 0]), np.isfinite(want[t:350, 0]))
+
+
+def test_padding_and_bad_ids_are_skipped():
+    case = Case("ids", 2, 1, 32, 32, (10, 20, 30, 40, 50), "bf16", resume="all")
+    q, k, v, dt, a, S = ins = scan_inputs(case)
+    cu, _, resume = packed(case)
+    seqs = torch.tensor([3, -1, 3, 99, 0], dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = torch.full((case.T, case.H, case.P), 7.0, device="cuda", dtype=case.dtype)
+    S1 = S.clone()
+    lar.prompt_scan(case.cfg(), S1, q, k, v, dt, a, cu, seqs=seqs, resume=resume, y=y, status=status)
+    assert status.item() == _abi.DEV_SEQS
+    live = check(case, ins, y, S1, *oracle(ins, cu, seqs, resume), cu, seqs, resume)
+    assert live.sum() == 60 and (y[torch.from_numpy(~live).cuda()] == 7).all()
+    status.zero_()
+    lar.prompt_scan(case.cfg(), S1, q, k, v, dt, a, cu, seqs=torch.tensor([3, -1, -1, 1, 0], dtype=torch.int32,
+                                                                          device="cuda"), status=status)
+    assert status.item() == 0  # padding alone is no error
+
+
+def test_bad_bounds_are_skipped():
+    case = Case("bounds", 2, 1, 32, 32, (10, 20, 30), "bf16")
+    q, k, v, dt, a, S = scan_inputs(case)
+    for bounds in ([0, 10, 5, 60], [-4, 10, 30, 60], [0, 10, 30, 61]):
+        cu = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        S1 = S.clone()
+        y = lar.prompt_scan(case.cfg(), S1, q, k, v, dt, a, cu, status=status)
+        assert status.item() == _abi.DEV_SEQS
+        bad = [i for i in range(3) if bounds[i] < 0 or bounds[i + 1] < bounds[i] or bounds[i + 1] > case.T]
+        for i in range(3):
+            assert torch.equal(S1[i], S[i]) == (i in bad)
+        assert y.shape == (case.T, case.H, case.P)
+
+
+def test_no_tokens_and_no_sequences():
+    case = Case("none", 2, 1, 32, 32, (0, 0), "bf16", resume="some")
+    q, k, v, dt, a, S = scan_inputs(case)
+    cu, seqs, resume = packed(case)
+    S1 = S.clone()
+    y = lar.prompt_scan(case.cfg(), S1, q, k, v, dt, a, cu, resume=resume)
+    assert y.shape[0] == 0 and torch.equal(S1[0], S[0]) and (S1[1] == 0).all()
+    S1 = S.clone()
+    lar.prompt_scan(case.cfg(), S1, q, k, v, dt, a, cu[:1])
+    assert torch.equal(S1, S)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_a_prompt_in_pieces_is_the_prompt(io):
+    """Fed in pieces through the state, a prompt ends where it ends fed at once: each way
+    within its bound of the oracle."""
+    whole = Case("whole", 4, 2, 64, 128, (700,), io)
+    ins = scan_inputs(whole)
+    q, k, v, dt, a, S = ins
+    S = S.clone()
+    on = torch.ones(1, dtype=torch.uint8, device="cuda")
+    ys, at = [], 0
+    for i, n in enumerate((300, 1, 128, 271)):
+        cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+        part = [t[at:at + n].contiguous() for t in (q, k, v, dt, a)]
+        ys.append(lar.prompt_scan(whole.cfg(), S, *part, cu, resume=on if i else None))
+        at += n
+    cu, seqs, resume = packed(whole)
+    check(whole, ins, torch.cat(ys), S, *oracle(ins, cu, seqs, resume), cu, seqs, resume)
+
+
+def test_scan_on_another_stream_and_in_a_graph():
+    case = Case("graph", 4, 2, 64, 128, (900, 33), "bf16", resume="all")
+    q, k, v, dt, a, S = ins = scan_inputs(case)
+    y0, S0, cu, seqs, resume = run(case, ins)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    S1 = S.clone()
+    torch.cuda.synchronize()
+    y1 = lar.prompt_scan(case.cfg(), S1, q, k, v, dt, a, cu, resume=resume, stream=side)
+    side.synchronize()
+    assert torch.equal(y0, y1) and torch.equal(S0, S1)
+    # two captured calls, replayed twice on new contents, with an eager call between
+    graphs, outs = [], []
+    Sg = [S.clone(), S.clone()]
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(lar.prompt_scan(case.cfg(), Sg[i], q, k, v, dt, a, cu, resume=resume))
+        graphs.append(g)
+    for _ in range(2):
+        for i in range(2):
+            Sg[i].copy_(S)
+        graphs[0].replay()
+        y2, S2, *_ = run(case, ins)
+        graphs[1].replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert torch.equal(outs[i], y0) and torch.equal(Sg[i], S0)
+        assert torch.equal(y2, y0) and torch.equal(S2, S0)
+    # other lengths in the same buffers
+    other = dataclasses.replace(case, lens=(33, 900))
+    cu.copy_(packed(other)[0])
+    Sg[0].copy_(S)
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    want, mag = oracle(ins, cu, None, resume)
+    check(other, ins, outs[0], Sg[0], want, mag, cu, None, resume)
