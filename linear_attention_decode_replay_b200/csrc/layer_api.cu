@@ -86,6 +86,11 @@ int check_scratch(const void* scratch, int64_t have, int64_t need) {
   return aligned(scratch, 256) ? REPLAY_OK : REPLAY_EALIGN;
 }
 
+int launch_scan(const ScanParams& p, int io, int sms, cudaStream_t s) {
+  if (io == REPLAY_BF16 && p.pk.tokens > 0) return launched(replay::launch_scan_tc(p, sms, s));
+  return launched(replay::launch_scan_serial(p, io, s));
+}
+
 }  // namespace
 
 extern "C" {
@@ -173,7 +178,7 @@ int replay_prompt_scan(const replay_config* cfg, int64_t tokens, const void* q, 
   if (n_seqs == 0) return REPLAY_OK;
   int sms;
   if ((rc = sm_count(&sms))) return rc;
-  return launched(replay::launch_scan(p, cfg->io, sms, stream_of(stream)));
+  return launch_scan(p, cfg->io, sms, stream_of(stream));
 }
 
 int64_t replay_prefill_scratch(const replay_ctx* ctx, int64_t tokens, int32_t n_seqs, int64_t max_len) {
@@ -204,7 +209,7 @@ int replay_prefill(replay_ctx* ctx, int64_t tokens, const void* q, const void* k
     if ((rc = replay_flush(ctx, mask, stream))) return rc;
   }
   p.counts = ctx->bufs.counts + (size_t)ctx->parity * c.batch;
-  if (replay::launch_scan(p, c.io, ctx->num_sms, s) != cudaSuccess) return REPLAY_ECUDA;
+  if ((rc = launch_scan(p, c.io, ctx->num_sms, s))) return rc;
   if (c.ckpt != REPLAY_CKPT_F32)
     return launched(replay::launch_refresh_copy(p.pk, c.heads, c.P, c.N, replay::ckpt_kind(c.ckpt), ctx->bufs.S0,
                                                 ctx->bufs.S0_codes, ctx->bufs.S0_scale, s));

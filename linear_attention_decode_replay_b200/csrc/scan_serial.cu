@@ -146,7 +146,7 @@ cudaError_t serial_io(const ScanParams& p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_scan(const ScanParams& p, int io, int num_sms, cudaStream_t s) {
+cudaError_t launch_scan_serial(const ScanParams& p, int io, cudaStream_t s) {
   return io == 1 ? serial_io<__nv_bfloat16>(p, s) : serial_io<float>(p, s);
 }
 
