@@ -20,23 +20,36 @@ namespace {
 
 constexpr int kChunk = 128;
 constexpr int kPT = 64;  // state rows of one block
-constexpr int kTcThreads = 320;
-// warps 0-3 (rows of C: P and the outputs), 4-7 (U and the state), 8 (TMA), 9 (MMA)
+constexpr int kTcThreads = 640;
+// Five warpgroups: 0 and 1 (rows of C, halves of the columns: P and the outputs), 2 (tokens:
+// decays and U), 3 (columns of the state), 4 (TMA and MMA). At 96 registers a thread at
+// launch, 2 and 4 give up what the state needs: (2 x 96 + 80 + 128 + 80) x 128 <= 5 x 96 x 128.
+constexpr int kWarpU = 8, kWarpS = 12, kWarpTma = 16, kWarpMmaQ = 17, kWarpMmaU = 18;
+constexpr int kRegsLaunch = 96, kRegsTokens = 80, kRegsState = 128, kRegsCopy = 80;
+static_assert(2 * kRegsLaunch + kRegsTokens + kRegsState + kRegsCopy <= 5 * kRegsLaunch, "registers moved, not made");
+constexpr int kSlots = 3;  // chunks whose decays are held
 
 struct alignas(64) ScanTcParams {
   CUtensorMap q, k, v;
   ScanParams s;
 };
 
-// tensor memory columns
-constexpr uint32_t kColC = 0, kColPhi = 128, kColPlo = 192, kColY1 = 256, kColY2 = 320, kColDS = 384;
+// Tensor memory columns. P lies over C: the two BF16 parts of 16 columns of P take the 16
+// columns that held C's.
+constexpr uint32_t kColC = 0, kColY1 = 128, kColY2 = 192, kColDS = 320;
 
 struct TcBars {
   uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t c_full, p_full, y_full, y_free, u_full, ds_full, s_full, tot_full, da_full[2], drain;
+  uint64_t c_full, p_full, y_full, y_free, u_full, ds_full, ds_free, s_full, da_full[kSlots], drain[2];
   uint32_t tmem, abort;
-  float total[2][4];  // the four warps' products of a
-  int bad[2];         // the chunk holds a v that is not finite
+};
+// the decays of one chunk; "block" is 32 tokens
+struct alignas(16) Decays {
+  float2 da[kChunk];  // a_{j+1}, Delta_j
+  float g[kChunk];    // Delta_j times the a after j in its block
+  float pre[kChunk];  // the a up to i in its block
+  float total[4];     // each block's product
+  int bad;            // the chunk holds a v that is not finite
 };
 
 template <int NT>
@@ -45,18 +58,24 @@ struct TcLayout {  // bytes from the 1024-byte aligned base
   static constexpr int kQK = NT / 64 * kTile;
   static constexpr int kSop = NT * 128;  // one part of the state operand: NT rows of 64 BF16
   static constexpr int q = 0, k = kQK, v = k + 2 * kQK, u = v + 2 * kTile, s = u + 3 * kTile;
-  static constexpr int da = s + 2 * kSop;                      // float2 [2][128]: a_{j+1}, Delta_j
-  static constexpr int abar = da + 2 * kChunk * 8;             // float [2][128]
-  static constexpr int bars = abar + 2 * kChunk * 4;
+  static constexpr int dec = s + 2 * kSop;
+  static constexpr int bars = dec + kSlots * (int)sizeof(Decays);
+  static_assert(dec % 16 == 0 && bars % 8 == 0, "vector reads of the decays, 8-byte barriers");
   static constexpr int bytes = bars + (int)sizeof(TcBars) + 1024;
 };
 
-// two floats' BF16 parts packed (a in the low half), and what remains of them
-__device__ __forceinline__ uint32_t take_part(float& a, float& b) {
+// two floats' BF16 parts packed (the first in the low half), and what remains of them
+__device__ __forceinline__ uint32_t take_part(f32x2& x) {
+  float a, b;
+  unpair(x, a, b);
   const uint32_t w = Vec<__nv_bfloat16>::pack2(a, b);
-  a -= __uint_as_float(w << 16);
-  b -= __uint_as_float(w & 0xFFFF0000u);
+  x = fma2(pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)), pair(-1.f, -1.f), x);
   return w;
+}
+__device__ __forceinline__ uint32_t last_part(f32x2 x) {
+  float a, b;
+  unpair(x, a, b);
+  return Vec<__nv_bfloat16>::pack2(a, b);
 }
 
 }  // namespace
@@ -68,24 +87,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   TcBars* bars = reinterpret_cast<TcBars*>(smem + Lay::bars);
-  float2* da = reinterpret_cast<float2*>(smem + Lay::da);
-  float* abar = reinterpret_cast<float*>(smem + Lay::abar);
+  Decays* dec = reinterpret_cast<Decays*>(smem + Lay::dec);
   const ScanParams& p = tp.s;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // values of the whole warp, told so to the compiler
+  auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+  const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1), mbar_init(&bars->q_empty, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars->k_full[i], 1), mbar_init(&bars->k_empty[i], 1);
-      mbar_init(&bars->v_full[i], 1), mbar_init(&bars->v_empty[i], 1);
-      mbar_init(&bars->da_full[i], 128);
-      bars->bad[i] = 0;
+      mbar_init(&bars->k_full[i], 1), mbar_init(&bars->k_empty[i], 2);
+      mbar_init(&bars->v_full[i], 1), mbar_init(&bars->v_empty[i], 256);
     }
-    mbar_init(&bars->c_full, 1), mbar_init(&bars->p_full, 128);
-    mbar_init(&bars->y_full, 1), mbar_init(&bars->y_free, 128);
-    mbar_init(&bars->u_full, 128), mbar_init(&bars->ds_full, 1), mbar_init(&bars->s_full, 128);
-    mbar_init(&bars->tot_full, 128), mbar_init(&bars->drain, 1);
+    mbar_init(&bars->c_full, 1), mbar_init(&bars->p_full, 256);
+    mbar_init(&bars->y_full, 1), mbar_init(&bars->y_free, 256);
+    mbar_init(&bars->u_full, 128), mbar_init(&bars->s_full, 128);
+    mbar_init(&bars->ds_full, 1), mbar_init(&bars->ds_free, 128);
+    for (int i = 0; i < kSlots; ++i) mbar_init(&bars->da_full[i], 128);
+    mbar_init(&bars->drain[0], 1), mbar_init(&bars->drain[1], 1);
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -101,56 +121,76 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
   if (!seq_bounds(p.pk, s, begin, end)) return;
   const int row = seq_row(p.pk, s);
   if (row < 0) return;
-  const int chunks = (int)((end - begin + kChunk - 1) / kChunk);
+  const int chunks = uniform((int)((end - begin + kChunk - 1) / kChunk));
 
-  if (warp == 9) tmem_alloc(&bars->tmem, 512);
+  if (warp == kWarpTma) tmem_alloc(&bars->tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bars->tmem;
+  const uint32_t tmem = uniform(bars->tmem);
   volatile uint32_t* abort = &bars->abort;
 
   // waits for a phase; false once any wait of the block has run out
   auto wait = [&](uint64_t* bar, int phase) -> bool {
-    const uint32_t parity = phase & 1;
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (true) {
-      if (mbar_try_wait(bar, parity)) return true;
-      if (*abort) return false;
-      if (clock64() - t0 > kWaitLimitCycles) {
+    int left = kPollLimit;
+    while (!mbar_poll(bar, phase & 1)) {
+      if (*abort || --left == 0) {
+        if (p.pk.status && !*abort) atomicOr(p.pk.status, kErrWaitTimeout);
         *abort = 1;
-        if (p.pk.status) atomicOr(p.pk.status, kErrWaitTimeout);
         return false;
       }
     }
+    return true;
   };
-
+  // two phases, tested together
+  auto wait2 = [&](uint64_t* bar0, int phase0, uint64_t* bar1, int phase1) -> bool {
+    const bool b0 = mbar_poll(bar0, phase0 & 1), b1 = mbar_poll(bar1, phase1 & 1);
+    return (b0 || wait(bar0, phase0)) && (b1 || wait(bar1, phase1));
+  };
   // the same for a whole warp: every lane goes on, or none
   auto wait_warp = [&](uint64_t* bar, int phase) { return __all_sync(0xffffffffu, wait(bar, phase)) != 0; };
+  auto wait2_warp = [&](uint64_t* bar0, int phase0, uint64_t* bar1, int phase1) {
+    return __all_sync(0xffffffffu, wait2(bar0, phase0, bar1, phase1)) != 0;
+  };
 
-  if (warp == 8) {
+  if (warp >= kWarpTma) {
+    regs_down<kRegsCopy>();
     // ------------------------------------------------------------ TMA
-    if (lane == 0) {
-      int c = 0, nq = 0, nk = 0, nv = 0;  // tiles issued
-      for (; c < chunks; ++c) {
+    if (warp == kWarpTma && lane == 0) {
+      // q of a chunk, then k and v of the next: the order in which their tiles fall free
+      int nq = 0, nk = 0, nv = 0;  // tiles issued
+      auto token = [&](int c) { return (int)(begin + (int64_t)c * kChunk); };
+      auto load_k = [&](int c) {
         const int b = c & 1;
-        const int t = (int)(begin + (int64_t)c * kChunk);
-        if (c >= 2 && !wait(&bars->k_empty[b], (c >> 1) - 1)) break;
+        if (c >= 2 && !wait(&bars->k_empty[b], (c >> 1) - 1)) return false;
         mbar_arrive_expect_tx(&bars->k_full[b], Lay::kQK);
         for (int i = 0; i < NT / 64; ++i)
-          tma_load3(smem + Lay::k + b * Lay::kQK + i * kTile, &tp.k, 64 * i, g, t, &bars->k_full[b]);
+          tma_load3(smem + Lay::k + b * Lay::kQK + i * kTile, &tp.k, 64 * i, g, token(c), &bars->k_full[b]);
         ++nk;
-        if (c >= 1 && !wait(&bars->q_empty, c - 1)) break;
+        return true;
+      };
+      auto load_v = [&](int c) {
+        const int b = c & 1;
+        if (c >= 2 && !wait(&bars->v_empty[b], (c >> 1) - 1)) return false;
+        mbar_arrive_expect_tx(&bars->v_full[b], kTile);
+        tma_load3(smem + Lay::v + b * kTile, &tp.v, p0, h, token(c), &bars->v_full[b]);
+        ++nv;
+        return true;
+      };
+      auto load_q = [&](int c) {
+        if (c >= 1 && !wait(&bars->q_empty, c - 1)) return false;
         mbar_arrive_expect_tx(&bars->q_full, Lay::kQK);
         for (int i = 0; i < NT / 64; ++i)
-          tma_load3(smem + Lay::q + i * kTile, &tp.q, 64 * i, g, t, &bars->q_full);
+          tma_load3(smem + Lay::q + i * kTile, &tp.q, 64 * i, g, token(c), &bars->q_full);
+        // q has one tile, so its next load starts late: from L2
+        if (c + 1 < chunks)
+          for (int i = 0; i < NT / 64; ++i) tma_prefetch3(&tp.q, 64 * i, g, token(c + 1));
         ++nq;
-        if (c >= 2 && !wait(&bars->v_empty[b], (c >> 1) - 1)) break;
-        mbar_arrive_expect_tx(&bars->v_full[b], kTile);
-        tma_load3(smem + Lay::v + b * kTile, &tp.v, p0, h, t, &bars->v_full[b]);
-        ++nv;
-      }
+        return true;
+      };
+      if (chunks > 0) load_k(0), load_v(0);
+      for (int c = 0; c < chunks; ++c)
+        if (!load_q(c) || (c + 1 < chunks && (!load_k(c + 1) || !load_v(c + 1)))) break;
       if (*abort) {  // no copy may land after the block has gone
         if (nq) mbar_wait_bounded(&bars->q_full, (nq - 1) & 1);
         for (int b = 0; b < 2; ++b) {
@@ -159,168 +199,210 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
         }
       }
     }
-  } else if (warp == 9) {
     // ------------------------------------------------------------ MMA
-    if (lane == 0) {
-      const uint32_t sq = smem_u32(smem + Lay::q), su = smem_u32(smem + Lay::u), ss = smem_u32(smem + Lay::s);
-      constexpr uint32_t kC = mma_idesc(128, 128, 0, 0), kY1 = mma_idesc(128, kPT, 0, 1);
-      constexpr uint32_t kDS2 = mma_idesc(128, 2 * kPT, 1, 1), kDS1 = mma_idesc(128, kPT, 1, 1);
+    // Two warps, since one that has issued a product goes on only once the product runs: with
+    // two the tensor cores have the next product at hand.
+    constexpr uint32_t kC = mma_idesc(128, 128, 0, 0), kY1 = mma_idesc(128, kPT, 0, 1);
+    constexpr uint32_t kY2 = mma_idesc(128, 2 * kPT, 0, 1), kDS = mma_idesc(128, 3 * kPT, 1, 1);
+    // operand tiles; a step of 16 of K is 32 bytes along a K-major row, 16 rows of an MN-major tile
+    if (warp == kWarpMmaQ) {
+      const uint64_t dq = smem_desc(smem_u32(smem + Lay::q), 16);
+      const uint64_t ds = smem_desc(smem_u32(smem + Lay::s), Lay::kSop);
       for (int c = 0; c < chunks; ++c) {
         const int b = c & 1;
-        const uint32_t sk = smem_u32(smem + Lay::k + b * Lay::kQK), sv = smem_u32(smem + Lay::v + b * kTile);
-        // C = Q K^T, once the last chunk's C has been read
-        if (!wait(&bars->q_full, c) || !wait(&bars->k_full[b], c >> 1)) break;
+        const uint64_t dk = smem_desc(smem_u32(smem + Lay::k + b * Lay::kQK), 16);
+        // C = Q K^T, once Y1 is done with the last chunk's P in the same columns
+        if (!wait2_warp(&bars->q_full, c, &bars->k_full[b], c >> 1)) break;
+        if (c >= 1 && !wait_warp(&bars->y_full, c - 1)) break;
         tc_fence_after();
-        for (int i = 0; i < NT / 16; ++i) {
-          const uint32_t at = i / 4 * kTile + i % 4 * 32;
-          mma_ss(tmem + kColC, smem_desc(sq + at, 16), smem_desc(sk + at, 16), kC, i > 0);
+        if (elect_lane()) {
+#pragma unroll
+          for (int i = 0; i < NT / 16; ++i) {
+            const int at = (i / 4 * kTile + i % 4 * 32) >> 4;
+            mma_ss(tmem + kColC, dq + at, dk + at, kC, i > 0);
+          }
+          mma_commit(&bars->c_full);
         }
-        mma_commit(&bars->c_full);
-        // Y2 = Q S^T, once the last chunk's outputs have been read
-        if (!wait(&bars->s_full, c) || (c >= 1 && !wait(&bars->y_free, c - 1))) break;
+        // Y2 = Q S^T, the state's two parts side by side, once the last chunk's outputs have been read
+        if (!wait_warp(&bars->s_full, c) || (c >= 1 && !wait_warp(&bars->y_free, c - 1))) break;
         tc_fence_after();
-        for (int part = 0; part < 2; ++part)
+        if (elect_lane()) {
+#pragma unroll
           for (int i = 0; i < NT / 16; ++i)
-            mma_ss(tmem + kColY2, smem_desc(sq + i / 4 * kTile + i % 4 * 32, 16),
-                   smem_desc(ss + part * Lay::kSop + i * 2048, 16), kY1, part + i > 0);
-        mma_commit(&bars->q_empty);
-        // dS = K^T U: the two larger parts side by side, the third onto the second
-        if (!wait(&bars->u_full, c)) break;
+            mma_ss(tmem + kColY2, dq + ((i / 4 * kTile + i % 4 * 32) >> 4), ds + i * 128, kY2, i > 0);
+          mma_commit(&bars->q_empty);
+          mma_commit(&bars->k_empty[b]);
+        }
+      }
+    } else if (warp == kWarpMmaU) {
+      const uint64_t du = smem_desc(smem_u32(smem + Lay::u), kTile);
+      for (int c = 0; c < chunks; ++c) {
+        const int b = c & 1;
+        const uint64_t dk = smem_desc(smem_u32(smem + Lay::k + b * Lay::kQK), kTile);
+        const uint64_t dv = smem_desc(smem_u32(smem + Lay::v + b * kTile), 16);
+        // dS = K^T U, the three parts side by side
+        if (!wait2_warp(&bars->u_full, c, &bars->k_full[b], c >> 1)) break;
+        if (c >= 1 && !wait_warp(&bars->ds_free, c - 1)) break;
         tc_fence_after();
-        for (int i = 0; i < kChunk / 16; ++i)
-          mma_ss(tmem + kColDS, smem_desc(sk + i * 2048, kTile), smem_desc(su + i * 2048, kTile), kDS2, i > 0);
-        for (int i = 0; i < kChunk / 16; ++i)
-          mma_ss(tmem + kColDS + kPT, smem_desc(sk + i * 2048, kTile), smem_desc(su + 2 * kTile + i * 2048, 16), kDS1,
-                 true);
-        mma_commit(&bars->ds_full);
-        mma_commit(&bars->k_empty[b]);
+        if (elect_lane()) {
+#pragma unroll
+          for (int i = 0; i < kChunk / 16; ++i) mma_ss(tmem + kColDS, dk + i * 128, du + i * 128, kDS, i > 0);
+          mma_commit(&bars->ds_full);
+          mma_commit(&bars->k_empty[b]);
+        }
         // Y1 = P V
-        if (!wait(&bars->p_full, c) || !wait(&bars->v_full[b], c >> 1)) break;
+        if (!wait2_warp(&bars->p_full, c, &bars->v_full[b], c >> 1)) break;
         tc_fence_after();
-        for (int part = 0; part < 2; ++part)
-          for (int i = 0; i < kChunk / 16; ++i)
-            mma_ts(tmem + kColY1, tmem + (part ? kColPlo : kColPhi) + i * 8, smem_desc(sv + i * 2048, 16), kY1,
-                   part + i > 0);
-        mma_commit(&bars->y_full);
-        mma_commit(&bars->v_empty[b]);
-      }
-      if (*abort) {  // nothing may still run on the tensor memory when it is freed
-        mma_commit(&bars->drain);
-        mbar_wait_bounded(&bars->drain, 0);
+        if (elect_lane()) {
+#pragma unroll
+          for (int i = 0; i < kChunk / 16; ++i) {
+            const uint32_t pa = tmem + kColC + i * 16;
+            mma_ts(tmem + kColY1, pa, dv + i * 128, kY1, i > 0);
+            mma_ts(tmem + kColY1, pa + 8, dv + i * 128, kY1, true);
+          }
+          mma_commit(&bars->y_full);
+        }
       }
     }
-  } else if (warp < 4) {
+    if (*abort && (warp == kWarpMmaQ || warp == kWarpMmaU)) {  // nothing may still run when the memory is freed
+      if (elect_lane()) mma_commit(&bars->drain[warp - kWarpMmaQ]);
+      mbar_wait_bounded(&bars->drain[warp - kWarpMmaQ], 0);
+    }
+  } else if (warp < kWarpU) {
     // ------------------------------------------------------------ P and the outputs: row i of the chunk
-    const int i = threadIdx.x;
-    const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
-    const uint32_t zero[16] = {0};
-    for (int cb = warp + 1; cb < 4; ++cb) {  // columns past the diagonal block stay zero
-      tmem_st16(tl + kColPhi + 16 * cb, zero);
-      tmem_st16(tl + kColPlo + 16 * cb, zero);
-    }
+    const int w4 = warp & 3, half = warp >> 2;
+    const int i = w4 * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(w4 * 32) << 16);
     for (int c = 0; c < chunks; ++c) {
       const int b = c & 1;
-      const int64_t t = begin + (int64_t)c * kChunk + i;
-      if (!wait_warp(&bars->da_full[b], c >> 1) || !wait_warp(&bars->c_full, c)) break;
+      const Decays& d = dec[c % kSlots];
+      if (!wait2_warp(&bars->da_full[c % kSlots], c / kSlots, &bars->c_full, c)) break;
       tc_fence_after();
-      const float4* dab = reinterpret_cast<const float4*>(da + b * kChunk);
-      float r = 0.f;
-      for (int cb = warp; cb >= 0; --cb) {
-        uint32_t x[32], hi[16], lo[16];
-        tmem_ld32(tl + kColC + 32 * cb, x);
-        tmem_wait_ld(x);
+      const float pre = d.pre[i];
+      // Half 0 takes the diagonal block of 32 columns, half 1 those before it. The loops stay small: four warps with code of their own
+      // share an instruction cache, and unrolled they waited for instructions.
+      if (half == 0) {
+        const float4* da = reinterpret_cast<const float4*>(d.da + 32 * w4);
+        float rd = 0.f;
+#pragma unroll 1
+        for (int j0 = 16; j0 >= 0; j0 -= 16) {  // products from j = i down
+          uint32_t x[16], hi[8], lo[8];
+          tmem_ld16(tl + kColC + 32 * w4 + j0, x);
+          tmem_wait_ld16(x);
 #pragma unroll
-        for (int jj = 30; jj >= 0; jj -= 2) {
-          const float4 d = dab[(32 * cb + jj) / 2];  // a_{j+1}, Delta_j, a_{j+2}, Delta_{j+1}
-          float p1, p0v;
-          if (cb == warp) {  // the diagonal block: r starts at j = i
-            r = jj + 1 == lane ? 1.f : r * d.z;
-            p1 = jj + 1 <= lane ? __uint_as_float(x[jj + 1]) * (r * d.w) : 0.f;
-            r = jj == lane ? 1.f : r * d.x;
-            p0v = jj <= lane ? __uint_as_float(x[jj]) * (r * d.y) : 0.f;
-          } else {
-            r *= d.z;
-            p1 = __uint_as_float(x[jj + 1]) * (r * d.w);
-            r *= d.x;
-            p0v = __uint_as_float(x[jj]) * (r * d.y);
+          for (int j = 14; j >= 0; j -= 2) {
+            const float4 u = da[(j0 + j) / 2];  // a_{j+1}, Delta_j, a_{j+2}, Delta_{j+1}
+            rd = j + 1 == lane - j0 ? 1.f : rd * u.z;
+            const float f1 = j + 1 <= lane - j0 ? __uint_as_float(x[j + 1]) * (rd * u.w) : 0.f;
+            rd = j == lane - j0 ? 1.f : rd * u.x;
+            const float f0 = j <= lane - j0 ? __uint_as_float(x[j]) * (rd * u.y) : 0.f;
+            f32x2 f = pair(f0, f1);
+            hi[j / 2] = take_part(f);
+            lo[j / 2] = last_part(f);
           }
-          hi[jj / 2] = take_part(p0v, p1);
-          lo[jj / 2] = Vec<__nv_bfloat16>::pack2(p0v, p1);
+          tmem_st8(tl + kColC + 32 * w4 + j0, hi);
+          tmem_st8(tl + kColC + 32 * w4 + j0 + 8, lo);
         }
-        tmem_st16(tl + kColPhi + 16 * cb, hi);
-        tmem_st16(tl + kColPlo + 16 * cb, lo);
+      } else {
+        const uint32_t zero[8] = {0};
+#pragma unroll 1
+        for (int x = 32 * (w4 + 1); x < kChunk; x += 8) tmem_st8(tl + kColC + x, zero);  // later tokens
+      }
+      float r = pre;  // from the block's end up to i
+#pragma unroll 1
+      for (int cb = half == 0 ? -1 : w4 - 1; cb >= 0; --cb) {
+        uint32_t x[32];
+        tmem_ld32(tl + kColC + 32 * cb, x);
+        const ulonglong2* gv = reinterpret_cast<const ulonglong2*>(d.g + 32 * cb);
+        const f32x2 rr = pair(r, r);
+        r *= d.total[cb];
+        tmem_wait_ld32(x);
+#pragma unroll
+        for (int j0 = 0; j0 < 32; j0 += 16) {
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const ulonglong2 e = gv[(j0 + j) / 4];
+            f32x2 f = mul2(pair(__uint_as_float(x[j0 + j]), __uint_as_float(x[j0 + j + 1])), mul2(rr, e.x));
+            hi[j / 2] = take_part(f);
+            lo[j / 2] = last_part(f);
+            f = mul2(pair(__uint_as_float(x[j0 + j + 2]), __uint_as_float(x[j0 + j + 3])), mul2(rr, e.y));
+            hi[j / 2 + 1] = take_part(f);
+            lo[j / 2 + 1] = last_part(f);
+          }
+          tmem_st8(tl + kColC + 32 * cb + j0, hi);
+          tmem_st8(tl + kColC + 32 * cb + j0 + 8, lo);
+        }
       }
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&bars->p_full);
 
-      if (!wait_warp(&bars->y_full, c)) break;
-      tc_fence_after();
-      const float ab = abar[b * kChunk + i];
-      const bool bad = bars->bad[b] != 0;
-      __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + ((size_t)t * p.H + h) * p.P + p0;
+      float abar = pre;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t y1[32], y2[32];
-        tmem_ld32(tl + kColY1 + 32 * half, y1);
-        tmem_ld32(tl + kColY2 + 32 * half, y2);
-        tmem_wait_ld(y1);
-        tmem_wait_ld(y2);
-        if (half == 1) {
+      for (int x = 0; x < 3; ++x)
+        if (x < w4) abar *= d.total[x];
+      // The outputs pass through the tile of v, which the products have read, so that their
+      // stores are whole sectors.
+      if (!wait2_warp(&bars->y_full, c, &bars->q_empty, c)) break;
+      tc_fence_after();
+      const bool bad = d.bad != 0;
+      uint8_t* tile = smem + Lay::v + b * kTile;
+      const int64_t t0 = begin + (int64_t)c * kChunk;
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part) {
+        uint32_t y1[16], y2[16], y3[16];
+        tmem_ld16(tl + kColY1 + 32 * half + 16 * part, y1);
+        tmem_ld16(tl + kColY2 + 32 * half + 16 * part, y2);
+        tmem_ld16(tl + kColY2 + kPT + 32 * half + 16 * part, y3);
+        tmem_wait_ld16(y1);
+        tmem_wait_ld16(y2);
+        tmem_wait_ld16(y3);
+        if (part == 1) {
           tc_fence_before();
           mbar_arrive(&bars->y_free);
         }
-        float o[32];
+        float o[16];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = fmaf(ab, __uint_as_float(y2[j]), __uint_as_float(y1[j]));
-        if (t < end) {
-          if (bad) {  // the products saw zeros in place of what is not finite in v: it reaches every later row
-            const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + p0 + 32 * half;
-            for (int j = 0; j <= i; ++j) {
-              const __nv_bfloat16* vj = v + ((size_t)(t - i + j) * p.H + h) * p.P;
+        for (int j = 0; j < 16; ++j)
+          o[j] = fmaf(abar, __uint_as_float(y2[j]) + __uint_as_float(y3[j]), __uint_as_float(y1[j]));
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (p0 + 32 * half + e < p.P) o[e] = fmaf(__bfloat162float(vj[e]), 0.f, o[e]);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 32; j += 8)
-            if (p0 + 32 * half + j < p.P)
-              *reinterpret_cast<uint4*>(y + 32 * half + j) = Vec<__nv_bfloat16>::pack(o + j);
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<uint4*>(tile + i * 128 + (((4 * half + 2 * part + e) ^ (i & 7)) << 4)) =
+              Vec<__nv_bfloat16>::pack(o + 8 * e);
+      }
+      if (bad && t0 + i < end) {
+        // the products saw zeros in place of what is not finite in v: it reaches every later row
+        const uint16_t* v = static_cast<const uint16_t*>(p.v) + p0;
+        for (int j = 0; j <= i; ++j) {
+          const uint16_t* vj = v + ((size_t)(t0 + j) * p.H + h) * p.P;
+          for (int e = 32 * half; e < 32 * half + 32 && p0 + e < p.P; ++e)
+            if ((vj[e] & 0x7F80) == 0x7F80)
+              *reinterpret_cast<uint16_t*>(tile + i * 128 + (((e / 8) ^ (i & 7)) << 4) + e % 8 * 2) = 0x7FC0;
         }
+      }
+      __syncwarp();
+      // eight rows of 64 bytes an instruction; rows r and r + 4 of a quarter warp lie on different banks
+      const int cx = 4 * half + (lane & 3), r0 = w4 * 32 + (lane >> 3) + (lane & 4);
+      uint4 out[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        out[e] = *reinterpret_cast<const uint4*>(tile + (r0 + 8 * e) * 128 + ((cx ^ (r0 & 7)) << 4));
+      fence_async_smem();
+      mbar_arrive(&bars->v_empty[b]);
+      if (p0 + 8 * cx < p.P) {
+        const int left = (int)(end - t0 < kChunk ? end - t0 : kChunk);
+        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + ((size_t)(t0 + r0) * p.H + h) * p.P + p0 + 8 * cx;
+        const size_t step = (size_t)8 * p.H * p.P;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (r0 + 8 * e < left) *reinterpret_cast<uint4*>(y + e * step) = out[e];
       }
     }
-  } else {
-    // ------------------------------------------------------------ U and the state: token j, then column n
-    const int j = threadIdx.x - 128, w4 = warp - 4;
-    const uint32_t tl = tmem + ((uint32_t)(w4 * 32) << 16);
-    const int n = j;
-    float S[kPT];
-    float* Sg = p.S + ((size_t)row * p.H + h) * p.P * p.N + n;
-    const bool res = p.pk.resume && p.pk.resume[s];
-#pragma unroll
-    for (int e = 0; e < kPT; ++e) S[e] = res && n < p.N && p0 + e < p.P ? Sg[(size_t)(p0 + e) * p.N] : 0.f;
-    // the state's two BF16 parts as an operand: row n, chunk x at x ^ (n % 8)
-    auto put_state = [&] {
-      if (n < NT) {
-        uint8_t* dst = smem + Lay::s + n * 128;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float f0 = S[8 * x + 2 * e], f1 = S[8 * x + 2 * e + 1];
-            hi[e] = take_part(f0, f1);
-            lo[e] = Vec<__nv_bfloat16>::pack2(f0, f1);
-          }
-          uint8_t* at = dst + ((x ^ (n & 7)) << 4);
-          *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(at + Lay::kSop) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-      }
-      fence_async_smem();
-      mbar_arrive(&bars->s_full);
-    };
+  } else if (warp < kWarpS) {
+    // ------------------------------------------------------------ decays and U: token j of the chunk
+    regs_down<kRegsTokens>();
+    const int j = threadIdx.x - 32 * kWarpU, w4 = warp - kWarpU;
     float a = 1.f, dt = 0.f;
     auto load_da = [&](int c) {  // this thread's token of chunk c; past the sequence: no decay, no step
       const int64_t t = begin + (int64_t)c * kChunk + j;
@@ -329,113 +411,166 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
       dt = in ? p.dt[(size_t)t * p.H + h] : 0.f;
     };
     load_da(0);
-    if (chunks > 0) put_state();
     for (int c = 0; c < chunks; ++c) {
       const int b = c & 1;
+      Decays& d = dec[c % kSlots];
       const int len = (int)(end - begin - (int64_t)c * kChunk < kChunk ? end - begin - (int64_t)c * kChunk : kChunk);
-      // products of the decays up to and after this token
+      // products of the decays up to and after this token, in its block and then over the chunk
       float pre = a, suf = a;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
-        const float u = __shfl_up_sync(0xffffffffu, pre, off), d = __shfl_down_sync(0xffffffffu, suf, off);
+        const float u = __shfl_up_sync(0xffffffffu, pre, off), f = __shfl_down_sync(0xffffffffu, suf, off);
         if (lane >= off) pre *= u;
-        if (lane + off < 32) suf *= d;
+        if (lane + off < 32) suf *= f;
       }
-      if (lane == 31) bars->total[b][w4] = pre;
       suf = __shfl_down_sync(0xffffffffu, suf, 1);
       if (lane == 31) suf = 1.f;
-      if (j == 0) bars->bad[b] = 0;
-      mbar_arrive(&bars->tot_full);
-      if (!wait_warp(&bars->tot_full, c)) break;
-      float all = 1.f;
+      if (lane == 31) d.total[w4] = pre;
+      if (j == 0) d.bad = 0;
+      d.pre[j] = pre;
+      d.g[j] = dt * suf;
+      d.da[j].y = dt;
+      if (j > 0) d.da[j - 1].x = a;
+      if (j == kChunk - 1) d.da[j].x = 1.f;
+      mbar_arrive(&bars->da_full[c % kSlots]);
+      if (!wait_warp(&bars->da_full[c % kSlots], c / kSlots)) break;
+      float wj = dt * suf;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float tx = bars->total[b][x];
-        all *= tx;
-        if (x < w4) pre *= tx;
-        if (x > w4) suf *= tx;
-      }
-      da[b * kChunk + j].y = dt;
-      if (j > 0) da[b * kChunk + j - 1].x = a;
-      if (j == kChunk - 1) da[b * kChunk + j].x = 1.f;
-      abar[b * kChunk + j] = pre;
-      mbar_arrive(&bars->da_full[b]);
-      const float wj = dt * suf;
+      for (int x = 1; x < 4; ++x)
+        if (x > w4) wj *= d.total[x];
       load_da(c + 1);
 
       if (!wait_warp(&bars->v_full[b], c >> 1)) break;
+      if (c >= 1 && !wait_warp(&bars->ds_full, c - 1)) break;  // U's last values have been read
       uint8_t* vrow = smem + Lay::v + b * kTile + j * 128;
       uint8_t* urow = smem + Lay::u + j * 128;
-      float check = 0.f;
-#pragma unroll
+      const f32x2 ww = pair(wj, wj);
+      f32x2 check[2] = {0, 0};  // 0 times what is not finite is NaN
+#pragma unroll 2
       for (int x = 0; x < 8; ++x) {
         const int at = (x ^ (j & 7)) << 4;
+        uint4 vu = *reinterpret_cast<const uint4*>(vrow + at);
+        if (j >= len) vu = make_uint4(0u, 0u, 0u, 0u);  // another sequence's tokens
         float f[8];
-        Vec<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(vrow + at), f);
+        Vec<__nv_bfloat16>::unpack(vu, f);
         uint32_t u1[4], u2[4], u3[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          check = fmaf(f[2 * e], 0.f, check);
-          check = fmaf(f[2 * e + 1], 0.f, check);
-          float f0 = j < len ? wj * f[2 * e] : 0.f, f1 = j < len ? wj * f[2 * e + 1] : 0.f;
-          u1[e] = take_part(f0, f1);
-          u2[e] = take_part(f0, f1);
-          u3[e] = Vec<__nv_bfloat16>::pack2(f0, f1);
+          const f32x2 v2 = pair(f[2 * e], f[2 * e + 1]);
+          check[e & 1] = fma2(v2, 0, check[e & 1]);
+          f32x2 u = mul2(v2, ww);
+          u1[e] = take_part(u);
+          u2[e] = take_part(u);
+          u3[e] = last_part(u);
         }
         *reinterpret_cast<uint4*>(urow + at) = make_uint4(u1[0], u1[1], u1[2], u1[3]);
         *reinterpret_cast<uint4*>(urow + kTile + at) = make_uint4(u2[0], u2[1], u2[2], u2[3]);
         *reinterpret_cast<uint4*>(urow + 2 * kTile + at) = make_uint4(u3[0], u3[1], u3[2], u3[3]);
       }
+      float c0, c1;
+      unpair(add2(check[0], check[1]), c0, c1);
       if (len < kChunk && !wait_warp(&bars->k_full[b], c >> 1)) break;
       if (j >= len) {
-        // another sequence's tokens: zeros in v and k (0 times its NaN would be NaN)
+        // zeros in their v and k too (0 times another sequence's NaN would be NaN)
         for (int x = 0; x < 8; ++x) *reinterpret_cast<uint4*>(vrow + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
         for (int i = 0; i < NT / 64; ++i)
           for (int x = 0; x < 8; ++x)
             *reinterpret_cast<uint4*>(smem + Lay::k + b * Lay::kQK + i * kTile + j * 128 + 16 * x) =
                 make_uint4(0u, 0u, 0u, 0u);
-      } else if (check != check) {
+      } else if (c0 + c1 != 0.f) {
         // what is not finite must not meet the zeros of the earlier tokens' rows of P
         for (int x = 0; x < 64; ++x) {
           uint16_t* e = reinterpret_cast<uint16_t*>(vrow) + x;
           if ((*e & 0x7F80) == 0x7F80) *e = 0;
         }
-        bars->bad[b] = 1;
+        d.bad = 1;
       }
       fence_async_smem();
       mbar_arrive(&bars->u_full);
-
-      if (!wait_warp(&bars->ds_full, c)) break;
+    }
+  } else if (warp < kWarpTma) {
+    // ------------------------------------------------------------ the state: column n
+    regs_up<kRegsState>();
+    const int n = threadIdx.x - 32 * kWarpS, w4 = warp - kWarpS;
+    const uint32_t tl = tmem + ((uint32_t)(w4 * 32) << 16);
+    f32x2 S[kPT / 2];
+    float* Sg = p.S + ((size_t)row * p.H + h) * p.P * p.N + n;
+    const bool res = p.pk.resume && p.pk.resume[s] && n < p.N;
+#pragma unroll
+    for (int e = 0; e < kPT; e += 2)
+      S[e / 2] = res && p0 + e < p.P ? pair(Sg[(size_t)(p0 + e) * p.N], Sg[(size_t)(p0 + e + 1) * p.N]) : 0;
+    // 16 rows p of the state's two BF16 parts as an operand: row n, chunk x at x ^ (n % 8)
+    uint8_t* dst = smem + Lay::s + n * 128;
+    auto put_state = [&](int part) {
+#pragma unroll
+      for (int x = 2 * part; x < 2 * part + 2; ++x) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          f32x2 f = S[4 * x + e];
+          hi[e] = take_part(f);
+          lo[e] = last_part(f);
+        }
+        uint8_t* at = dst + ((x ^ (n & 7)) << 4);
+        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(at + Lay::kSop) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+    };
+    if (n < NT) {
+#pragma unroll
+      for (int part = 0; part < 4; ++part) put_state(part);
+    }
+    fence_async_smem();
+    mbar_arrive(&bars->s_full);
+    for (int c = 0; c < chunks; ++c) {
+      // dS is there, and Y2 has read the state's operand
+      if (!wait2_warp(&bars->ds_full, c, &bars->q_empty, c)) break;
       tc_fence_after();
+      const float* tot = dec[c % kSlots].total;
+      const float all = (tot[0] * tot[1]) * (tot[2] * tot[3]);
+      const f32x2 all2 = pair(all, all);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t d1[32], d2[32];
-        tmem_ld32(tl + kColDS + 32 * half, d1);
-        tmem_ld32(tl + kColDS + kPT + 32 * half, d2);
-        tmem_wait_ld(d1);
-        tmem_wait_ld(d2);
+      for (int part = 0; part < 4; ++part) {
+        uint32_t d1[16], d2[16], d3[16];
+        tmem_ld16(tl + kColDS + 16 * part, d1);
+        tmem_ld16(tl + kColDS + kPT + 16 * part, d2);
+        tmem_ld16(tl + kColDS + 2 * kPT + 16 * part, d3);
+        tmem_wait_ld16(d1);
+        tmem_wait_ld16(d2);
+        tmem_wait_ld16(d3);
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          S[32 * half + e] = fmaf(all, S[32 * half + e], __uint_as_float(d1[e]) + __uint_as_float(d2[e]));
+        for (int e = 0; e < 16; e += 2) {
+          const f32x2 f2 = pair(__uint_as_float(d2[e]), __uint_as_float(d2[e + 1]));
+          const f32x2 f3 = pair(__uint_as_float(d3[e]), __uint_as_float(d3[e + 1]));
+          const f32x2 f1 = pair(__uint_as_float(d1[e]), __uint_as_float(d1[e + 1]));
+          f32x2& x = S[8 * part + e / 2];
+          x = fma2(all2, x, add2(f1, add2(f2, f3)));
+        }
+        if (n < NT) put_state(part);
       }
       tc_fence_before();
-      if (c + 1 < chunks) {
-        if (!wait_warp(&bars->q_empty, c)) break;  // Y2 has read the state before
-        put_state();
-      }
+      mbar_arrive(&bars->ds_free);
+      fence_async_smem();
+      mbar_arrive(&bars->s_full);
     }
     if (!*abort) {
 #pragma unroll
-      for (int e = 0; e < kPT; ++e)
-        if (n < p.N && p0 + e < p.P) Sg[(size_t)(p0 + e) * p.N] = S[e];
-      if (p.counts && h == 0 && p0 == 0 && j == 0) p.counts[row] = 0;
+      for (int e = 0; e < kPT; e += 2) {  // P is a multiple of 8
+        float s0, s1;
+        unpair(S[e / 2], s0, s1);
+        if (n < p.N && p0 + e < p.P) {
+          Sg[(size_t)(p0 + e) * p.N] = s0;
+          Sg[(size_t)(p0 + e + 1) * p.N] = s1;
+        }
+      }
+      if (p.counts && h == 0 && p0 == 0 && n == 0) p.counts[row] = 0;
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_free(tmem, 512);
+  if (warp == kWarpTma) tmem_free(tmem, 512);
 }
 
 namespace {
