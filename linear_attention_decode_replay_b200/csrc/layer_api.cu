@@ -78,6 +78,8 @@ int scan_params(ScanParams* p, const replay_config& c, int64_t tokens, const voi
   p->H = c.heads, p->G = c.groups, p->P = c.P, p->N = c.N;
   p->q = q, p->k = k, p->v = v, p->dt = dt, p->a = a, p->S = S, p->y = y;
   p->counts = nullptr;
+  p->seg_tokens = p->max_segs = 0;
+  p->seg_state = p->seg_decay = nullptr;
   return REPLAY_OK;
 }
 
@@ -86,9 +88,25 @@ int check_scratch(const void* scratch, int64_t have, int64_t need) {
   return aligned(scratch, 256) ? REPLAY_OK : REPLAY_EALIGN;
 }
 
-int launch_scan(const ScanParams& p, int io, int sms, cudaStream_t s) {
-  if (io == REPLAY_BF16 && p.pk.tokens > 0) return launched(replay::launch_scan_tc(p, sms, s));
-  return launched(replay::launch_scan_serial(p, io, s));
+// The scratch of one scan: the segments' states, then their decays.
+bool on_tensor_cores(const replay_config& c, int64_t tokens) { return c.io == REPLAY_BF16 && tokens > 0; }
+int64_t segment_units(const replay_config& c, const replay::ScanSplit& sp) {
+  return (int64_t)sp.max_segs * c.heads * ((c.P + 63) / 64);
+}
+int64_t scan_scratch(const replay_config& c, int64_t tokens, int32_t n_seqs, int64_t max_len) {
+  if (!on_tensor_cores(c, tokens)) return 0;
+  const replay::ScanSplit sp = replay::scan_split(tokens, n_seqs, max_len, c.heads, c.P);
+  const int64_t units = sp.seg_tokens ? segment_units(c, sp) : 0;
+  return round256(units * 64 * c.N * 4) + round256(units * 4);
+}
+
+int launch_scan(ScanParams& p, const replay_config& c, int64_t max_len, void* scratch, cudaStream_t s) {
+  if (!on_tensor_cores(c, p.pk.tokens)) return launched(replay::launch_scan_serial(p, c.io, s));
+  const replay::ScanSplit sp = replay::scan_split(p.pk.tokens, p.pk.n_seqs, max_len, c.heads, c.P);
+  p.seg_tokens = sp.seg_tokens, p.max_segs = sp.max_segs;
+  p.seg_state = static_cast<float*>(scratch);
+  p.seg_decay = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + round256(segment_units(c, sp) * 64 * c.N * 4));
+  return launched(replay::launch_scan_tc(p, s));
 }
 
 }  // namespace
@@ -160,7 +178,8 @@ int64_t replay_prompt_scan_scratch(const replay_config* cfg, int64_t tokens, int
   const int rc = replay::validate_config(cfg, false);
   if (rc) return rc;
   if (tokens < 0 || tokens > kMaxTokens || n_seqs < 0 || max_len < 0) return REPLAY_EINVAL;
-  return 0;
+  if ((int64_t)n_seqs * cfg->heads > INT32_MAX / 4) return REPLAY_EINVAL;
+  return scan_scratch(*cfg, tokens, n_seqs, max_len);
 }
 
 int replay_prompt_scan(const replay_config* cfg, int64_t tokens, const void* q, const void* k, const void* v,
@@ -176,15 +195,13 @@ int replay_prompt_scan(const replay_config* cfg, int64_t tokens, const void* q, 
   if (need < 0) return (int)need;
   if ((rc = check_scratch(scratch, scratch_bytes, need))) return rc;
   if (n_seqs == 0) return REPLAY_OK;
-  int sms;
-  if ((rc = sm_count(&sms))) return rc;
-  return launch_scan(p, cfg->io, sms, stream_of(stream));
+  return launch_scan(p, *cfg, max_len, scratch, stream_of(stream));
 }
 
 int64_t replay_prefill_scratch(const replay_ctx* ctx, int64_t tokens, int32_t n_seqs, int64_t max_len) {
   if (!ctx) return REPLAY_EINVAL;
   const int64_t n = replay_prompt_scan_scratch(&ctx->cfg, tokens, n_seqs, max_len);
-  return n < 0 ? n : n + round256(ctx->cfg.batch);
+  return n < 0 ? n : round256(ctx->cfg.batch) + n;
 }
 
 int replay_prefill(replay_ctx* ctx, int64_t tokens, const void* q, const void* k, const void* v, const float* dt,
@@ -209,7 +226,7 @@ int replay_prefill(replay_ctx* ctx, int64_t tokens, const void* q, const void* k
     if ((rc = replay_flush(ctx, mask, stream))) return rc;
   }
   p.counts = ctx->bufs.counts + (size_t)ctx->parity * c.batch;
-  if ((rc = launch_scan(p, c.io, ctx->num_sms, s))) return rc;
+  if ((rc = launch_scan(p, c, max_len, static_cast<uint8_t*>(scratch) + round256(c.batch), s))) return rc;
   if (c.ckpt != REPLAY_CKPT_F32)
     return launched(replay::launch_refresh_copy(p.pk, c.heads, c.P, c.N, replay::ckpt_kind(c.ckpt), ctx->bufs.S0,
                                                 ctx->bufs.S0_codes, ctx->bufs.S0_scale, s));

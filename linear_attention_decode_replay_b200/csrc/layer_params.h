@@ -45,7 +45,18 @@ struct ScanParams {
   void* y;
   float* S;         // [batch][H][P][N]
   int32_t* counts;  // a decode layer's pointer words (set empty for the served rows), or null
+  // long sequences in segments of seg_tokens (0: whole): [segment][head][block of 64 rows p]
+  // states of 64 x N floats, each segment's own and then the one it starts from, and decays
+  int32_t seg_tokens, max_segs;
+  float *seg_state, *seg_decay;
 };
+
+// How the tensor-core scan splits its work: tokens of a segment (0 = sequences whole) and the
+// most segments there can be.
+struct ScanSplit {
+  int32_t seg_tokens, max_segs;
+};
+ScanSplit scan_split(int64_t tokens, int32_t n_seqs, int64_t max_len, int H, int P);
 
 struct NormParams {
   int64_t rows;
@@ -63,7 +74,7 @@ struct NormParams {
 cudaError_t launch_prompt_inputs(const InputsParams& p, int io, int num_sms, cudaStream_t s);
 cudaError_t launch_token_inputs(const InputsParams& p, int io, int num_sms, cudaStream_t s);
 cudaError_t launch_scan_serial(const ScanParams& p, int io, cudaStream_t s);
-cudaError_t launch_scan_tc(const ScanParams& p, int num_sms, cudaStream_t s);  // BF16
+cudaError_t launch_scan_tc(const ScanParams& p, cudaStream_t s);  // BF16, tokens > 0
 // a decode layer's prefill: mask[b] = 1 where a sequence resumes row b; the read copy of
 // the served rows requantised from their checkpoints
 cudaError_t launch_resume_mask(const Packed& pk, uint8_t* mask, cudaStream_t s);

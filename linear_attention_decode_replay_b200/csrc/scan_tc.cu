@@ -19,7 +19,8 @@ namespace replay {
 namespace {
 
 constexpr int kChunk = 128;
-constexpr int kPT = 64;  // state rows of one block
+constexpr int kPT = 64;        // state rows of one block
+constexpr int kSplitSms = 148;  // the SMs that a split aims to fill
 constexpr int kTcThreads = 640;
 // Five warpgroups: 0 and 1 (rows of C, halves of the columns: P and the outputs), 2 (tokens:
 // decays and U), 3 (columns of the state), 4 (TMA and MMA). At 96 registers a thread at
@@ -32,6 +33,7 @@ constexpr int kSlots = 3;  // chunks whose decays are held
 struct alignas(64) ScanTcParams {
   CUtensorMap q, k, v;
   ScanParams s;
+  int wide_y;  // rows of y start on 32-byte boundaries
 };
 
 // Tensor memory columns. P lies over C: the two BF16 parts of 16 columns of P take the 16
@@ -78,9 +80,51 @@ __device__ __forceinline__ uint32_t last_part(f32x2 x) {
   return Vec<__nv_bfloat16>::pack2(a, b);
 }
 
+// two registers of a load from tensor memory as a pair
+__device__ __forceinline__ f32x2 reg_pair(const uint32_t* r) {
+  return pair(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+// 32 bytes, a whole sector, in one store (the address 32-byte aligned)
+__device__ __forceinline__ void store_sector(void* dst, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 }  // namespace
 
-template <int NT>
+// Segment number `seg` of the packed sequences' segments: its sequence, its place among the
+// sequence's, and how many those are. Whole warps; false past the last segment.
+__device__ __forceinline__ bool find_segment(const Packed& pk, int seg_tokens, int seg, int& s, int& m, int& of) {
+  const int lane = threadIdx.x & 31;
+  int before = 0;
+  for (int s0 = 0; s0 < pk.n_seqs; s0 += 32) {
+    int n = 0;
+    if (s0 + lane < pk.n_seqs) {
+      const int64_t len = (int64_t)pk.cu[s0 + lane + 1] - pk.cu[s0 + lane];
+      n = len > seg_tokens && len <= pk.tokens ? (int)((len + seg_tokens - 1) / seg_tokens) : 1;
+    }
+    int upto = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += u;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, before + upto > seg);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      s = s0 + l;
+      of = __shfl_sync(0xffffffffu, n, l);
+      m = seg - (before + __shfl_sync(0xffffffffu, upto - n, l));
+      return s < pk.n_seqs;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return false;
+}
+
+// LOCAL: only the segments' own states, from zero, for those with a segment behind them.
+template <int NT, bool LOCAL>
 __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_constant__ ScanTcParams tp) {
   using Lay = TcLayout<NT>;
   constexpr int kTile = Lay::kTile;
@@ -97,8 +141,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1), mbar_init(&bars->q_empty, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars->k_full[i], 1), mbar_init(&bars->k_empty[i], 2);
-      mbar_init(&bars->v_full[i], 1), mbar_init(&bars->v_empty[i], 256);
+      mbar_init(&bars->k_full[i], 1), mbar_init(&bars->k_empty[i], LOCAL ? 1 : 2);
+      mbar_init(&bars->v_full[i], 1), mbar_init(&bars->v_empty[i], LOCAL ? 128 : 1);
     }
     mbar_init(&bars->c_full, 1), mbar_init(&bars->p_full, 256);
     mbar_init(&bars->y_full, 1), mbar_init(&bars->y_free, 256);
@@ -111,14 +155,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // the block's unit: sequence, head, block of 64 state rows
+  // the block's unit: sequence or segment of one, head, block of 64 state rows
   const int ptiles = (p.P + kPT - 1) / kPT;
   const int unit = blockIdx.x;
-  const int s = unit / (p.H * ptiles);
   const int h = unit / ptiles % p.H, g = h / (p.H / p.G);
   const int p0 = unit % ptiles * kPT;
+  int s = unit / (p.H * ptiles), seg = 0, segs = 1;
+  if (p.seg_tokens && !find_segment(p.pk, p.seg_tokens, s, s, seg, segs)) return;
+  if (LOCAL && seg == segs - 1) return;
   int64_t begin, end;
   if (!seq_bounds(p.pk, s, begin, end)) return;
+  if (segs > 1) {
+    begin += (int64_t)seg * p.seg_tokens;
+    if (seg < segs - 1) end = begin + p.seg_tokens;
+  }
   const int row = seq_row(p.pk, s);
   if (row < 0) return;
   const int chunks = uniform((int)((end - begin + kChunk - 1) / kChunk));
@@ -130,12 +180,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
   const uint32_t tmem = uniform(bars->tmem);
   volatile uint32_t* abort = &bars->abort;
 
-  // waits for a phase; false once any wait of the block has run out
+  // waits for a phase; false if it takes too long (the block then winds down: every other
+  // wait of its ends within the same time)
   auto wait = [&](uint64_t* bar, int phase) -> bool {
     int left = kPollLimit;
+#pragma unroll 1
     while (!mbar_poll(bar, phase & 1)) {
-      if (*abort || --left == 0) {
-        if (p.pk.status && !*abort) atomicOr(p.pk.status, kErrWaitTimeout);
+      if (--left == 0) {
         *abort = 1;
         return false;
       }
@@ -159,38 +210,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
     if (warp == kWarpTma && lane == 0) {
       // q of a chunk, then k and v of the next: the order in which their tiles fall free
       int nq = 0, nk = 0, nv = 0;  // tiles issued
-      auto token = [&](int c) { return (int)(begin + (int64_t)c * kChunk); };
-      auto load_k = [&](int c) {
-        const int b = c & 1;
-        if (c >= 2 && !wait(&bars->k_empty[b], (c >> 1) - 1)) return false;
-        mbar_arrive_expect_tx(&bars->k_full[b], Lay::kQK);
-        for (int i = 0; i < NT / 64; ++i)
-          tma_load3(smem + Lay::k + b * Lay::kQK + i * kTile, &tp.k, 64 * i, g, token(c), &bars->k_full[b]);
-        ++nk;
-        return true;
-      };
-      auto load_v = [&](int c) {
-        const int b = c & 1;
-        if (c >= 2 && !wait(&bars->v_empty[b], (c >> 1) - 1)) return false;
-        mbar_arrive_expect_tx(&bars->v_full[b], kTile);
-        tma_load3(smem + Lay::v + b * kTile, &tp.v, p0, h, token(c), &bars->v_full[b]);
-        ++nv;
-        return true;
-      };
-      auto load_q = [&](int c) {
-        if (c >= 1 && !wait(&bars->q_empty, c - 1)) return false;
-        mbar_arrive_expect_tx(&bars->q_full, Lay::kQK);
-        for (int i = 0; i < NT / 64; ++i)
-          tma_load3(smem + Lay::q + i * kTile, &tp.q, 64 * i, g, token(c), &bars->q_full);
-        // q has one tile, so its next load starts late: from L2
-        if (c + 1 < chunks)
-          for (int i = 0; i < NT / 64; ++i) tma_prefetch3(&tp.q, 64 * i, g, token(c + 1));
-        ++nq;
-        return true;
-      };
-      if (chunks > 0) load_k(0), load_v(0);
-      for (int c = 0; c < chunks; ++c)
-        if (!load_q(c) || (c + 1 < chunks && (!load_k(c + 1) || !load_v(c + 1)))) break;
+#pragma unroll 1
+      for (int c = -1; c < chunks; ++c) {
+        const int t = (int)(begin + (int64_t)c * kChunk);
+        if (!LOCAL && c >= 0) {
+          if (c >= 1 && !wait(&bars->q_empty, c - 1)) break;
+          mbar_arrive_expect_tx(&bars->q_full, Lay::kQK);
+#pragma unroll 1
+          for (int i = 0; i < NT / 64; ++i) {
+            tma_load3(smem + Lay::q + i * kTile, &tp.q, 64 * i, g, t, &bars->q_full);
+            // q has one tile, so its next load starts late: from L2
+            if (c + 1 < chunks) tma_prefetch3(&tp.q, 64 * i, g, t + kChunk);
+          }
+          ++nq;
+        }
+        const int n = c + 1, b = n & 1;
+        if (n < chunks) {
+          if (n >= 2 && !wait(&bars->k_empty[b], (n >> 1) - 1)) break;
+          mbar_arrive_expect_tx(&bars->k_full[b], Lay::kQK);
+#pragma unroll 1
+          for (int i = 0; i < NT / 64; ++i)
+            tma_load3(smem + Lay::k + b * Lay::kQK + i * kTile, &tp.k, 64 * i, g, t + kChunk, &bars->k_full[b]);
+          ++nk;
+          if (n >= 2 && !wait(&bars->v_empty[b], (n >> 1) - 1)) break;
+          mbar_arrive_expect_tx(&bars->v_full[b], kTile);
+          tma_load3(smem + Lay::v + b * kTile, &tp.v, p0, h, t + kChunk, &bars->v_full[b]);
+          ++nv;
+        }
+      }
       if (*abort) {  // no copy may land after the block has gone
         if (nq) mbar_wait_bounded(&bars->q_full, (nq - 1) & 1);
         for (int b = 0; b < 2; ++b) {
@@ -205,9 +252,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
     constexpr uint32_t kC = mma_idesc(128, 128, 0, 0), kY1 = mma_idesc(128, kPT, 0, 1);
     constexpr uint32_t kY2 = mma_idesc(128, 2 * kPT, 0, 1), kDS = mma_idesc(128, 3 * kPT, 1, 1);
     // operand tiles; a step of 16 of K is 32 bytes along a K-major row, 16 rows of an MN-major tile
-    if (warp == kWarpMmaQ) {
+    if (!LOCAL && warp == kWarpMmaQ) {
       const uint64_t dq = smem_desc(smem_u32(smem + Lay::q), 16);
       const uint64_t ds = smem_desc(smem_u32(smem + Lay::s), Lay::kSop);
+#pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
         const int b = c & 1;
         const uint64_t dk = smem_desc(smem_u32(smem + Lay::k + b * Lay::kQK), 16);
@@ -216,7 +264,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
         if (c >= 1 && !wait_warp(&bars->y_full, c - 1)) break;
         tc_fence_after();
         if (elect_lane()) {
-#pragma unroll
+#pragma unroll 2
           for (int i = 0; i < NT / 16; ++i) {
             const int at = (i / 4 * kTile + i % 4 * 32) >> 4;
             mma_ss(tmem + kColC, dq + at, dk + at, kC, i > 0);
@@ -227,7 +275,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
         if (!wait_warp(&bars->s_full, c) || (c >= 1 && !wait_warp(&bars->y_free, c - 1))) break;
         tc_fence_after();
         if (elect_lane()) {
-#pragma unroll
+#pragma unroll 2
           for (int i = 0; i < NT / 16; ++i)
             mma_ss(tmem + kColY2, dq + ((i / 4 * kTile + i % 4 * 32) >> 4), ds + i * 128, kY2, i > 0);
           mma_commit(&bars->q_empty);
@@ -236,6 +284,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
       }
     } else if (warp == kWarpMmaU) {
       const uint64_t du = smem_desc(smem_u32(smem + Lay::u), kTile);
+#pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
         const int b = c & 1;
         const uint64_t dk = smem_desc(smem_u32(smem + Lay::k + b * Lay::kQK), kTile);
@@ -245,22 +294,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
         if (c >= 1 && !wait_warp(&bars->ds_free, c - 1)) break;
         tc_fence_after();
         if (elect_lane()) {
-#pragma unroll
+#pragma unroll 2
           for (int i = 0; i < kChunk / 16; ++i) mma_ss(tmem + kColDS, dk + i * 128, du + i * 128, kDS, i > 0);
           mma_commit(&bars->ds_full);
           mma_commit(&bars->k_empty[b]);
         }
+        if (LOCAL) continue;
         // Y1 = P V
         if (!wait2_warp(&bars->p_full, c, &bars->v_full[b], c >> 1)) break;
         tc_fence_after();
         if (elect_lane()) {
-#pragma unroll
+#pragma unroll 2
           for (int i = 0; i < kChunk / 16; ++i) {
             const uint32_t pa = tmem + kColC + i * 16;
             mma_ts(tmem + kColY1, pa, dv + i * 128, kY1, i > 0);
             mma_ts(tmem + kColY1, pa + 8, dv + i * 128, kY1, true);
           }
           mma_commit(&bars->y_full);
+          mma_commit(&bars->v_empty[b]);
         }
       }
     }
@@ -273,8 +324,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
     const int w4 = warp & 3, half = warp >> 2;
     const int i = w4 * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(w4 * 32) << 16);
-    for (int c = 0; c < chunks; ++c) {
-      const int b = c & 1;
+#pragma unroll 1
+    for (int c = 0; c < (LOCAL ? 0 : chunks); ++c) {
       const Decays& d = dec[c % kSlots];
       if (!wait2_warp(&bars->da_full[c % kSlots], c / kSlots, &bars->c_full, c)) break;
       tc_fence_after();
@@ -342,16 +393,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
 #pragma unroll
       for (int x = 0; x < 3; ++x)
         if (x < w4) abar *= d.total[x];
-      // The outputs pass through the tile of v, which the products have read, so that their
-      // stores are whole sectors.
       if (!wait2_warp(&bars->y_full, c, &bars->q_empty, c)) break;
       tc_fence_after();
       const bool bad = d.bad != 0;
-      uint8_t* tile = smem + Lay::v + b * kTile;
-      const int64_t t0 = begin + (int64_t)c * kChunk;
+      const int64_t t = begin + (int64_t)c * kChunk + i;
+      __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + ((size_t)t * p.H + h) * p.P + p0 + 32 * half;
+      const f32x2 ab = pair(abar, abar);
 #pragma unroll 1
       for (int part = 0; part < 2; ++part) {
-        uint32_t y1[16], y2[16], y3[16];
+        uint32_t y1[16], y2[16], y3[16], o[8];
         tmem_ld16(tl + kColY1 + 32 * half + 16 * part, y1);
         tmem_ld16(tl + kColY2 + 32 * half + 16 * part, y2);
         tmem_ld16(tl + kColY2 + kPT + 32 * half + 16 * part, y3);
@@ -362,41 +412,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
           tc_fence_before();
           mbar_arrive(&bars->y_free);
         }
-        float o[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          o[j] = fmaf(abar, __uint_as_float(y2[j]) + __uint_as_float(y3[j]), __uint_as_float(y1[j]));
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<uint4*>(tile + i * 128 + (((4 * half + 2 * part + e) ^ (i & 7)) << 4)) =
-              Vec<__nv_bfloat16>::pack(o + 8 * e);
-      }
-      if (bad && t0 + i < end) {
-        // the products saw zeros in place of what is not finite in v: it reaches every later row
-        const uint16_t* v = static_cast<const uint16_t*>(p.v) + p0;
-        for (int j = 0; j <= i; ++j) {
-          const uint16_t* vj = v + ((size_t)(t0 + j) * p.H + h) * p.P;
-          for (int e = 32 * half; e < 32 * half + 32 && p0 + e < p.P; ++e)
-            if ((vj[e] & 0x7F80) == 0x7F80)
-              *reinterpret_cast<uint16_t*>(tile + i * 128 + (((e / 8) ^ (i & 7)) << 4) + e % 8 * 2) = 0x7FC0;
+        for (int j = 0; j < 16; j += 2)
+          o[j / 2] = last_part(fma2(ab, add2(reg_pair(y2 + j), reg_pair(y3 + j)), reg_pair(y1 + j)));
+        const int left = t < end ? p.P - (p0 + 32 * half + 16 * part) : 0;  // of the head's rows p
+        if (left >= 16 && tp.wide_y) {
+          store_sector(y + 16 * part, o);
+        } else {
+          if (left > 0) *reinterpret_cast<uint4*>(y + 16 * part) = make_uint4(o[0], o[1], o[2], o[3]);
+          if (left > 8) *reinterpret_cast<uint4*>(y + 16 * part + 8) = make_uint4(o[4], o[5], o[6], o[7]);
         }
       }
-      __syncwarp();
-      // eight rows of 64 bytes an instruction; rows r and r + 4 of a quarter warp lie on different banks
-      const int cx = 4 * half + (lane & 3), r0 = w4 * 32 + (lane >> 3) + (lane & 4);
-      uint4 out[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        out[e] = *reinterpret_cast<const uint4*>(tile + (r0 + 8 * e) * 128 + ((cx ^ (r0 & 7)) << 4));
-      fence_async_smem();
-      mbar_arrive(&bars->v_empty[b]);
-      if (p0 + 8 * cx < p.P) {
-        const int left = (int)(end - t0 < kChunk ? end - t0 : kChunk);
-        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + ((size_t)(t0 + r0) * p.H + h) * p.P + p0 + 8 * cx;
-        const size_t step = (size_t)8 * p.H * p.P;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (r0 + 8 * e < left) *reinterpret_cast<uint4*>(y + e * step) = out[e];
+      if (bad && t < end) {
+        // the products saw zeros in place of what is not finite in v: it reaches every later row
+        const uint16_t* v = static_cast<const uint16_t*>(p.v) + p0 + 32 * half;
+#pragma unroll 1
+        for (int j = 0; j <= i; ++j) {
+          const uint16_t* vj = v + ((size_t)(t - i + j) * p.H + h) * p.P;
+#pragma unroll 1
+          for (int e = 0; e < 32 && p0 + 32 * half + e < p.P; ++e)
+            if ((vj[e] & 0x7F80) == 0x7F80) reinterpret_cast<uint16_t*>(y)[e] = 0x7FC0;
+        }
       }
     }
   } else if (warp < kWarpS) {
@@ -411,6 +447,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
       dt = in ? p.dt[(size_t)t * p.H + h] : 0.f;
     };
     load_da(0);
+#pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
       const int b = c & 1;
       Decays& d = dec[c % kSlots];
@@ -444,13 +481,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
       if (c >= 1 && !wait_warp(&bars->ds_full, c - 1)) break;  // U's last values have been read
       uint8_t* vrow = smem + Lay::v + b * kTile + j * 128;
       uint8_t* urow = smem + Lay::u + j * 128;
+      if (len < kChunk && !wait_warp(&bars->k_full[b], c >> 1)) break;
+      if (j >= len) {
+        // another sequence's tokens: zeros in v and k (0 times its NaN would be NaN)
+        for (int x = 0; x < 8; ++x) *reinterpret_cast<uint4*>(vrow + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < NT / 64; ++i)
+          for (int x = 0; x < 8; ++x)
+            *reinterpret_cast<uint4*>(smem + Lay::k + b * Lay::kQK + i * kTile + j * 128 + 16 * x) =
+                make_uint4(0u, 0u, 0u, 0u);
+      }
       const f32x2 ww = pair(wj, wj);
       f32x2 check[2] = {0, 0};  // 0 times what is not finite is NaN
 #pragma unroll 2
       for (int x = 0; x < 8; ++x) {
         const int at = (x ^ (j & 7)) << 4;
-        uint4 vu = *reinterpret_cast<const uint4*>(vrow + at);
-        if (j >= len) vu = make_uint4(0u, 0u, 0u, 0u);  // another sequence's tokens
+        const uint4 vu = *reinterpret_cast<const uint4*>(vrow + at);
         float f[8];
         Vec<__nv_bfloat16>::unpack(vu, f);
         uint32_t u1[4], u2[4], u3[4];
@@ -469,16 +514,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
       }
       float c0, c1;
       unpair(add2(check[0], check[1]), c0, c1);
-      if (len < kChunk && !wait_warp(&bars->k_full[b], c >> 1)) break;
-      if (j >= len) {
-        // zeros in their v and k too (0 times another sequence's NaN would be NaN)
-        for (int x = 0; x < 8; ++x) *reinterpret_cast<uint4*>(vrow + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
-        for (int i = 0; i < NT / 64; ++i)
-          for (int x = 0; x < 8; ++x)
-            *reinterpret_cast<uint4*>(smem + Lay::k + b * Lay::kQK + i * kTile + j * 128 + 16 * x) =
-                make_uint4(0u, 0u, 0u, 0u);
-      } else if (c0 + c1 != 0.f) {
+      if (!LOCAL && c0 + c1 != 0.f) {
         // what is not finite must not meet the zeros of the earlier tokens' rows of P
+#pragma unroll 1
         for (int x = 0; x < 64; ++x) {
           uint16_t* e = reinterpret_cast<uint16_t*>(vrow) + x;
           if ((*e & 0x7F80) == 0x7F80) *e = 0;
@@ -487,6 +525,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
       }
       fence_async_smem();
       mbar_arrive(&bars->u_full);
+      if (LOCAL) mbar_arrive(&bars->v_empty[b]);
     }
   } else if (warp < kWarpTma) {
     // ------------------------------------------------------------ the state: column n
@@ -494,11 +533,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
     const int n = threadIdx.x - 32 * kWarpS, w4 = warp - kWarpS;
     const uint32_t tl = tmem + ((uint32_t)(w4 * 32) << 16);
     f32x2 S[kPT / 2];
-    float* Sg = p.S + ((size_t)row * p.H + h) * p.P * p.N + n;
-    const bool res = p.pk.resume && p.pk.resume[s] && n < p.N;
+    // rows p of the state that it starts from: the caller's, a segment's, or zero
+    float* Sg = p.S + (((size_t)row * p.H + h) * p.P + p0) * p.N + n;
+    float* Eg = p.seg_state + (size_t)unit * kPT * p.N + n;
+    const float* from = segs > 1 ? Eg : Sg;
+    const bool res = !LOCAL && n < p.N && (segs > 1 || (p.pk.resume && p.pk.resume[s]));
 #pragma unroll
-    for (int e = 0; e < kPT; e += 2)
-      S[e / 2] = res && p0 + e < p.P ? pair(Sg[(size_t)(p0 + e) * p.N], Sg[(size_t)(p0 + e + 1) * p.N]) : 0;
+    for (int e = 0; e < kPT; e += 2)  // P is a multiple of 8
+      S[e / 2] = res && p0 + e < p.P ? pair(from[(size_t)e * p.N], from[(size_t)(e + 1) * p.N]) : 0;
+    float decay = 1.f;
     // 16 rows p of the state's two BF16 parts as an operand: row n, chunk x at x ^ (n % 8)
     uint8_t* dst = smem + Lay::s + n * 128;
     auto put_state = [&](int part) {
@@ -516,19 +559,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
         *reinterpret_cast<uint4*>(at + Lay::kSop) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
     };
-    if (n < NT) {
+    if (!LOCAL && n < NT) {
 #pragma unroll
       for (int part = 0; part < 4; ++part) put_state(part);
     }
     fence_async_smem();
     mbar_arrive(&bars->s_full);
+#pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
       // dS is there, and Y2 has read the state's operand
-      if (!wait2_warp(&bars->ds_full, c, &bars->q_empty, c)) break;
+      if (LOCAL ? !wait_warp(&bars->ds_full, c) : !wait2_warp(&bars->ds_full, c, &bars->q_empty, c)) break;
       tc_fence_after();
       const float* tot = dec[c % kSlots].total;
       const float all = (tot[0] * tot[1]) * (tot[2] * tot[3]);
       const f32x2 all2 = pair(all, all);
+      if (LOCAL) decay *= all;
 #pragma unroll
       for (int part = 0; part < 4; ++part) {
         uint32_t d1[16], d2[16], d3[16];
@@ -540,37 +585,92 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
         tmem_wait_ld16(d3);
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
-          const f32x2 f2 = pair(__uint_as_float(d2[e]), __uint_as_float(d2[e + 1]));
-          const f32x2 f3 = pair(__uint_as_float(d3[e]), __uint_as_float(d3[e + 1]));
-          const f32x2 f1 = pair(__uint_as_float(d1[e]), __uint_as_float(d1[e + 1]));
           f32x2& x = S[8 * part + e / 2];
-          x = fma2(all2, x, add2(f1, add2(f2, f3)));
+          x = fma2(all2, x, add2(reg_pair(d1 + e), add2(reg_pair(d2 + e), reg_pair(d3 + e))));
         }
-        if (n < NT) put_state(part);
+        if (!LOCAL && n < NT) put_state(part);
       }
       tc_fence_before();
       mbar_arrive(&bars->ds_free);
       fence_async_smem();
       mbar_arrive(&bars->s_full);
     }
-    if (!*abort) {
+    if (!*abort && (LOCAL || seg == segs - 1)) {
+      float* to = LOCAL ? Eg : Sg;
 #pragma unroll
-      for (int e = 0; e < kPT; e += 2) {  // P is a multiple of 8
+      for (int e = 0; e < kPT; e += 2) {
         float s0, s1;
         unpair(S[e / 2], s0, s1);
         if (n < p.N && p0 + e < p.P) {
-          Sg[(size_t)(p0 + e) * p.N] = s0;
-          Sg[(size_t)(p0 + e + 1) * p.N] = s1;
+          to[(size_t)e * p.N] = s0;
+          to[(size_t)(e + 1) * p.N] = s1;
         }
       }
-      if (p.counts && h == 0 && p0 == 0 && n == 0) p.counts[row] = 0;
+      if (LOCAL && n == 0) p.seg_decay[unit] = decay;
+      if (!LOCAL && p.counts && h == 0 && p0 == 0 && n == 0) p.counts[row] = 0;
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (*abort && p.pk.status && threadIdx.x == 0) atomicOr(p.pk.status, kErrWaitTimeout);
   if (warp == kWarpTma) tmem_free(tmem, 512);
+}
+
+constexpr int kCarryAhead = 8;  // segments whose loads are in flight together
+
+// The state that each segment starts from, in place of the segments' own: for the sequences
+// of more than one segment, from the caller's row (or zero) on, S <- decay S + own. A block
+// takes one sequence's head, a thread four columns of a row.
+__global__ void __launch_bounds__(256) scan_carry_kernel(const __grid_constant__ ScanParams p) {
+  pdl_enter();
+  const int h = blockIdx.x % p.H;
+  const int s = blockIdx.x / p.H;
+  int64_t begin, end;
+  if (!seq_bounds(p.pk, s, begin, end)) return;
+  const int segs = (int)((end - begin + p.seg_tokens - 1) / p.seg_tokens);
+  if (segs <= 1) return;
+  const int row = seq_row(p.pk, s);
+  if (row < 0) return;
+  // segments before this sequence's
+  int first = 0;
+  for (int e = threadIdx.x & 31; e < s; e += 32) {
+    const int64_t len = (int64_t)p.pk.cu[e + 1] - p.pk.cu[e];
+    first += len > p.seg_tokens && len <= p.pk.tokens ? (int)((len + p.seg_tokens - 1) / p.seg_tokens) : 1;
+  }
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) first += __shfl_xor_sync(0xffffffffu, first, off);
+  if (first + segs > p.max_segs) return;  // only where bounds are out of order
+  const int ptiles = (p.P + kPT - 1) / kPT;
+  const bool res = p.pk.resume && p.pk.resume[s];
+  const int vecs = p.P * p.N / 4;
+  for (int i = blockIdx.y * 256 + threadIdx.x; i < vecs; i += gridDim.y * 256) {
+    const int r = i * 4 / p.N, col = i * 4 % p.N;
+    const int pt = r / kPT;
+    float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (res) S = *reinterpret_cast<const float4*>(p.S + (((size_t)row * p.H + h) * p.P + r) * p.N + col);
+    const size_t step = (size_t)p.H * ptiles;
+    const size_t unit0 = ((size_t)first * p.H + h) * ptiles + pt;
+    float4* at = reinterpret_cast<float4*>(p.seg_state + (unit0 * kPT + r % kPT) * p.N + col);
+    const size_t hop = step * kPT * p.N / 4;
+    for (int m0 = 0; m0 < segs; m0 += kCarryAhead) {
+      float4 own[kCarryAhead];
+      float d[kCarryAhead];
+#pragma unroll
+      for (int u = 0; u < kCarryAhead; ++u) {
+        const bool in = m0 + u < segs - 1;  // the last segment's own state is not needed
+        own[u] = in ? at[(m0 + u) * hop] : make_float4(0.f, 0.f, 0.f, 0.f);
+        d[u] = in ? p.seg_decay[unit0 + (m0 + u) * step] : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < kCarryAhead; ++u) {
+        if (m0 + u < segs) at[(m0 + u) * hop] = S;
+        S = make_float4(fmaf(d[u], S.x, own[u].x), fmaf(d[u], S.y, own[u].y), fmaf(d[u], S.z, own[u].z),
+                        fmaf(d[u], S.w, own[u].w));
+      }
+    }
+  }
 }
 
 namespace {
@@ -603,7 +703,7 @@ bool tile_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int w
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NT>
+template <int NT, bool LOCAL>
 cudaError_t launch_tc(const ScanTcParams& tp, int64_t units, cudaStream_t s) {
   constexpr int smem = TcLayout<NT>::bytes;
   static bool configured[64] = {false};  // per device; setting it twice does no harm
@@ -611,23 +711,55 @@ cudaError_t launch_tc(const ScanTcParams& tp, int64_t units, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !configured[dev]) {
-    e = cudaFuncSetAttribute(scan_tc_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(scan_tc_kernel<NT, LOCAL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) configured[dev] = true;
   }
-  return pdl_launch(scan_tc_kernel<NT>, dim3((unsigned)units), kTcThreads, smem, s, tp);
+  return pdl_launch(scan_tc_kernel<NT, LOCAL>, dim3((unsigned)units), kTcThreads, smem, s, tp);
+}
+
+template <int NT>
+cudaError_t launch_scan_nt(const ScanTcParams& tp, cudaStream_t s) {
+  const ScanParams& p = tp.s;
+  const int64_t heads = (int64_t)p.H * ((p.P + kPT - 1) / kPT);
+  if (!p.seg_tokens) return launch_tc<NT, false>(tp, p.pk.n_seqs * heads, s);
+  cudaError_t e = launch_tc<NT, true>(tp, p.max_segs * heads, s);
+  if (e != cudaSuccess) return e;
+  e = pdl_launch(scan_carry_kernel, dim3((unsigned)((int64_t)p.pk.n_seqs * p.H), (p.P * p.N / 4 + 255) / 256), 256, 0, s,
+                 tp.s);
+  return e != cudaSuccess ? e : launch_tc<NT, false>(tp, p.max_segs * heads, s);
 }
 
 }  // namespace
 
-cudaError_t launch_scan_tc(const ScanParams& p, int num_sms, cudaStream_t s) {
+ScanSplit scan_split(int64_t tokens, int32_t n_seqs, int64_t max_len, int H, int P) {
+  if (tokens <= 0 || n_seqs <= 0) return {0, 0};
+  const int64_t heads = (int64_t)H * ((P + kPT - 1) / kPT);
+  const int64_t chunks = tokens / kChunk + n_seqs;  // about
+  const int64_t longest = ((max_len > 0 && max_len < tokens ? max_len : tokens) + kChunk - 1) / kChunk;
+  // Times in chunks of one block. Whole sequences: the SMs' share and, since the blocks do not
+  // end together, half of the longest. Segments of n chunks: waves of n and a block's start
+  // (2) each, 1.5 times for the segments' own states, and the launches (6).
+  const int64_t whole = 2 * (chunks * heads / kSplitSms) + longest + 4;
+  int64_t best = 0, seg = 0;
+  for (int64_t n = 2; n < longest; n += n < 32 ? 1 : n / 16) {
+    const int64_t units = (tokens / (n * kChunk) + n_seqs) * heads;
+    if (units > INT32_MAX / 4) continue;
+    const int64_t cost = 3 * ((units + kSplitSms - 1) / kSplitSms) * (n + 2) + 12;
+    if (!seg || cost < best) best = cost, seg = n;
+  }
+  if (!seg || whole <= best) return {0, 0};
+  return {(int32_t)(seg * kChunk), (int32_t)(tokens / (seg * kChunk) + n_seqs)};
+}
+
+cudaError_t launch_scan_tc(const ScanParams& p, cudaStream_t s) {
   ScanTcParams tp;
   tp.s = p;
+  tp.wide_y = p.P % 16 == 0 && reinterpret_cast<uintptr_t>(p.y) % 32 == 0;
   if (!tile_map(&tp.q, p.q, p.pk.tokens, p.G, p.N) || !tile_map(&tp.k, p.k, p.pk.tokens, p.G, p.N) ||
       !tile_map(&tp.v, p.v, p.pk.tokens, p.H, p.P))
     return cudaErrorInvalidValue;
-  const int64_t units = (int64_t)p.pk.n_seqs * p.H * ((p.P + kPT - 1) / kPT);
-  return p.N > 64 ? launch_tc<128>(tp, units, s) : launch_tc<64>(tp, units, s);
+  return p.N > 64 ? launch_scan_nt<128>(tp, s) : launch_scan_nt<64>(tp, s);
 }
 
 }  // namespace replay

@@ -39,6 +39,8 @@ CASES = [
     Case("f32_n64_p40", 2, 1, 40, 64, (33, 131), "f32"),
     Case("many_short", 4, 2, 64, 128, tuple(1 + i % 5 for i in range(70)), "bf16", resume="some", rows=80),
     Case("long", 2, 1, 64, 128, (5003,), "bf16", resume="all"),
+    Case("long_several", 2, 2, 128, 128, (2900, 0, 1, 2561, 256, 129), "bf16", resume="some", rows=9, lead=4, tail=9),
+    Case("long_n64", 3, 1, 24, 64, (1, 2000, 3333), "bf16", resume="some", rows=3),
     Case("long_f32", 1, 1, 32, 64, (3001, 40), "f32"),
 ]
 
