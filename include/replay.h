@@ -377,7 +377,7 @@ int replay_verify_static_scratch(replay_ctx* ctx, int32_t n_pos, const void* q, 
  * where the sequence is shorter).
  *   x:    device [tokens] rows of D io, ldx apart     raw: [tokens] rows of H io, ldr apart
  *   w:    device [width][D] FP32, width 2..4 (w[width - 1] takes the token itself)
- *   bias: [D] FP32 or NULL   dt_bias: [H] FP32 or NULL   A: [H] FP32
+ *   bias: [D] FP32 or NULL (w and bias 16-byte aligned)   dt_bias: [H] FP32 or NULL   A: [H] FP32
  *   conv: device [batch][width - 1][D] io, oldest row first (updated)
  *   q, k: device [tokens][G][N] io   v: [tokens][H][P] io   dt, a: [tokens][H] FP32 (written)
  * No output may overlap x, raw or conv. */
@@ -446,7 +446,7 @@ int replay_prefill(replay_ctx* ctx, int64_t tokens, const void* q, const void* k
  * the mean over each of norm_groups equal parts of a row of H*P (a multiple of 8 each).
  *   y: device [rows][H][P], FP32 or io (y_type: a replay_dtype)   z: [rows] rows of H*P io, ldz apart
  *   v: device [rows][H][P] io and D: [H] FP32, or both NULL (no skip term)
- *   weight: device [H*P] FP32   out: device [rows][H*P] io (written; may be z or v, or a y
+ *   weight: device [H*P] FP32, 16-byte aligned   out: device [rows][H*P] io (written; may be z or v, or a y
  *   of the same type, itself, where that is dense) */
 int replay_gated_norm(const replay_config* cfg, int64_t rows, const void* y, int32_t y_type, const void* z,
                       int64_t ldz, const void* v, const float* D, const float* weight, int32_t norm_groups,

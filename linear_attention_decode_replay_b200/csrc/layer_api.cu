@@ -60,7 +60,7 @@ int inputs_params(InputsParams* p, const replay_config& c, int32_t width, int64_
   if (ldx < D || ldr < c.heads) return REPLAY_EINVAL;
   const int s = io_bytes(c);
   if (!aligned(x, 16) || (ldx * s) % 16 || !aligned(conv, 16) || !aligned(raw, s)) return REPLAY_EALIGN;
-  if (!aligned(w, 4) || !aligned(bias, 4) || !aligned(dt_bias, 4) || !aligned(A, 4)) return REPLAY_EALIGN;
+  if (!aligned(w, 16) || !aligned(bias, 16) || !aligned(dt_bias, 4) || !aligned(A, 4)) return REPLAY_EALIGN;
   *p = InputsParams{};
   p->H = c.heads, p->G = c.groups, p->P = c.P, p->N = c.N, p->D = (int32_t)D, p->width = width;
   p->x = x, p->ldx = ldx, p->raw = raw, p->ldr = ldr;
@@ -241,17 +241,17 @@ int replay_gated_norm(const replay_config* cfg, int64_t rows, const void* y, int
   const int64_t width = (int64_t)cfg->heads * cfg->P;
   if (rows < 0 || width > INT32_MAX || norm_groups < 1 || width % norm_groups || (width / norm_groups) % 8)
     return REPLAY_EINVAL;
-  if (rows > INT32_MAX / norm_groups) return REPLAY_EINVAL;
+  if (width / 8 * (cfg->P / 8) >= INT32_MAX || rows > INT32_MAX / norm_groups) return REPLAY_EINVAL;
   if (y_type != REPLAY_F32 && y_type != cfg->io) return REPLAY_EINVAL;
   if (!weight || (!v) != (!D) || ldz < width || !(eps >= 0.f)) return REPLAY_EINVAL;
   if (rows > 0 && (!y || !z || !out)) return REPLAY_EINVAL;
   if (!aligned(y, 16) || !aligned(z, 16) || (ldz * io_bytes(*cfg)) % 16 || !aligned(v, 16) || !aligned(out, 16) ||
-      !aligned(D, 4) || !aligned(weight, 4))
+      !aligned(D, 4) || !aligned(weight, 16))
     return REPLAY_EALIGN;
   if (rows == 0) return REPLAY_OK;
   int sms;
   if ((rc = sm_count(&sms))) return rc;
-  NormParams p{rows, cfg->heads, cfg->P, norm_groups, y, z, ldz, v, D, weight, eps, out};
+  NormParams p{rows, cfg->heads, cfg->P, norm_groups, y, z, ldz, v, D, weight, eps, out, 0u};
   return launched(replay::launch_gated_norm(p, cfg->io, y_type, sms, stream_of(stream)));
 }
 

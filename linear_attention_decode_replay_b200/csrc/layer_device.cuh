@@ -9,12 +9,21 @@ namespace replay {
 
 constexpr int32_t kErrSeqs = 1 << 4;  // a bad or repeated row id, or sequence bounds out of order
 
-// A vector of 16 bytes of inputs: 4 floats or 8 BF16.
-template <typename IO>
+// A vector of inputs, 16 bytes: 4 floats or 8 BF16; or 4 BF16 in 8 bytes.
+__device__ __forceinline__ uint32_t bf16_pack2(float lo, float hi) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+__device__ __forceinline__ void bf16_unpack2(uint32_t w, float* f) {  // a BF16 is the upper half of its FP32
+  f[0] = __uint_as_float(w << 16);
+  f[1] = __uint_as_float(w & 0xFFFF0000u);
+}
+template <typename IO, int N = 16 / sizeof(IO)>
 struct Vec;
 template <>
-struct Vec<float> {
+struct Vec<float, 4> {
   static constexpr int n = 4;
+  using raw = uint4;
   __device__ __forceinline__ static void unpack(uint4 u, float* f) {
     f[0] = __uint_as_float(u.x);
     f[1] = __uint_as_float(u.y);
@@ -24,26 +33,49 @@ struct Vec<float> {
   __device__ __forceinline__ static uint4 pack(const float* f) {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
   }
+  __device__ __forceinline__ static uint4 zero() { return make_uint4(0u, 0u, 0u, 0u); }
 };
 template <>
-struct Vec<__nv_bfloat16> {
+struct Vec<__nv_bfloat16, 8> {
   static constexpr int n = 8;
+  using raw = uint4;
   __device__ __forceinline__ static void unpack(uint4 u, float* f) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {  // a BF16 is the upper half of the FP32 of the same value
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    bf16_unpack2(u.x, f);
+    bf16_unpack2(u.y, f + 2);
+    bf16_unpack2(u.z, f + 4);
+    bf16_unpack2(u.w, f + 6);
   }
-  __device__ __forceinline__ static uint32_t pack2(float lo, float hi) {
-    const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&t);
-  }
+  __device__ __forceinline__ static uint32_t pack2(float lo, float hi) { return bf16_pack2(lo, hi); }
   __device__ __forceinline__ static uint4 pack(const float* f) {
     return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
   }
+  __device__ __forceinline__ static uint4 zero() { return make_uint4(0u, 0u, 0u, 0u); }
 };
+template <>
+struct Vec<__nv_bfloat16, 4> {
+  static constexpr int n = 4;
+  using raw = uint2;
+  __device__ __forceinline__ static void unpack(uint2 u, float* f) {
+    bf16_unpack2(u.x, f);
+    bf16_unpack2(u.y, f + 2);
+  }
+  __device__ __forceinline__ static uint2 pack(const float* f) {
+    return make_uint2(bf16_pack2(f[0], f[1]), bf16_pack2(f[2], f[3]));
+  }
+  __device__ __forceinline__ static uint2 zero() { return make_uint2(0u, 0u); }
+};
+// x sigmoid(x). For BF16 results the hardware's exponential and reciprocal, each within a
+// few units of 2^-23 (the result's own rounding is 2^-9); for FP32 results the accurate ones.
+template <typename IO>
+__device__ __forceinline__ float silu(float x) {
+  if constexpr (sizeof(IO) == 2) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return x * r;
+  }
+  return x / (1.f + expf(-x));
+}
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 

@@ -12,14 +12,6 @@ namespace {
 
 constexpr int kThreadsIn = 128;
 
-// x sigmoid(x). BF16 results take the fast exponential and division (relative error about
-// 2^-21, against the result's own rounding of 2^-9); FP32 results the accurate ones.
-template <typename IO>
-__device__ __forceinline__ float silu(float x) {
-  if constexpr (sizeof(IO) == 2) return __fdividef(x, 1.f + __expf(-x));
-  return x / (1.f + expf(-x));
-}
-
 // Delta and a of one head from the raw step size; softplus(x) = max(x, 0) + log1p(e^-|x|)
 // holds for every x.
 __device__ __forceinline__ void step_size(float x, float A, float& dt, float& a) {
@@ -28,22 +20,28 @@ __device__ __forceinline__ void step_size(float x, float A, float& dt, float& a)
   a = expf(-dt * A);
 }
 
+// Channels of one thread: four, so that a block's loads in flight need few registers.
+constexpr int kChannels = 4;
+
 template <typename IO, int W>
 struct Filter {
-  static constexpr int V = Vec<IO>::n;
+  using Vc = Vec<IO, kChannels>;
+  static constexpr int V = kChannels;
   float w[W][V], b[V];
   __device__ __forceinline__ void load(const InputsParams& p, int c0) {
+    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 bb = p.bias ? *reinterpret_cast<const float4*>(p.bias + c0) : z;
+    b[0] = bb.x, b[1] = bb.y, b[2] = bb.z, b[3] = bb.w;
 #pragma unroll
-    for (int j = 0; j < V; ++j) b[j] = p.bias ? p.bias[c0 + j] : 0.f;
-#pragma unroll
-    for (int i = 0; i < W; ++i)
-#pragma unroll
-      for (int j = 0; j < V; ++j) w[i][j] = p.w[(size_t)i * p.D + c0 + j];
+    for (int i = 0; i < W; ++i) {
+      const float4 ww = *reinterpret_cast<const float4*>(p.w + (size_t)i * p.D + c0);
+      w[i][0] = ww.x, w[i][1] = ww.y, w[i][2] = ww.z, w[i][3] = ww.w;
+    }
   }
   // the output of `x` after the rows `hist`, which it then joins
-  __device__ __forceinline__ uint4 step(float (*hist)[V], uint4 xu) const {
+  __device__ __forceinline__ typename Vc::raw step(float (*hist)[V], typename Vc::raw xu) const {
     float x[V], o[V];
-    Vec<IO>::unpack(xu, x);
+    Vc::unpack(xu, x);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       float acc = b[j];
@@ -54,7 +52,7 @@ struct Filter {
       for (int i = 0; i + 1 < W - 1; ++i) hist[i][j] = hist[i + 1][j];
       hist[W - 2][j] = x[j];
     }
-    return Vec<IO>::pack(o);
+    return Vc::pack(o);
   }
 };
 
@@ -81,8 +79,10 @@ __device__ __forceinline__ Dest dest_of(const InputsParams& p, int c0) {
 // that the thread that writes a state element is the only one that reads it.
 template <typename IO, int W>
 __global__ void __launch_bounds__(kThreadsIn) prompt_inputs_kernel(const __grid_constant__ InputsParams p) {
-  constexpr int V = Vec<IO>::n, K = W - 1;
-  constexpr int U = 4;  // tokens whose loads are in flight together
+  using Vc = Vec<IO, kChannels>;
+  using Raw = typename Vc::raw;
+  constexpr int V = kChannels, K = W - 1;
+  constexpr int U = 8;  // tokens whose loads are in flight together
   pdl_enter();
   const Packed& pk = p.pk;
   const int64_t t0 = (int64_t)blockIdx.x * p.tile;
@@ -100,14 +100,20 @@ __global__ void __launch_bounds__(kThreadsIn) prompt_inputs_kernel(const __grid_
   }
   const uint8_t* x = static_cast<const uint8_t*>(p.x) + (size_t)c0 * sizeof(IO);
   const size_t xs = (size_t)p.ldx * sizeof(IO);
-  auto x_at = [&](int64_t t) { return __ldg(reinterpret_cast<const uint4*>(x + (size_t)t * xs)); };
+  auto x_at = [&](int64_t t) { return __ldg(reinterpret_cast<const Raw*>(x + (size_t)t * xs)); };
 
-  // the first sequence that starts in this tile or after it
+  // the first sequence that starts in this tile or after it: 32 bounds at a time
   int lo = 0, hi = pk.n_seqs;
   while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (pk.cu[mid] < t0) lo = mid + 1;
-    else hi = mid;
+    const int hop = (hi - lo + 31) / 32, at = lo + (int)(threadIdx.x & 31) * hop;
+    const int n = __popc(__ballot_sync(0xffffffffu, at < hi && __ldg(pk.cu + (at < hi ? at : lo)) < t0));
+    if (hop == 1) {
+      lo += n;
+      break;
+    }
+    if (n == 0) break;
+    hi = lo + n * hop < hi ? lo + n * hop : hi;
+    lo += (n - 1) * hop + 1;
   }
   for (int s = lo > 0 ? lo - 1 : 0; s < pk.n_seqs; ++s) {
     const bool owner = s >= lo;
@@ -133,19 +139,19 @@ __global__ void __launch_bounds__(kThreadsIn) prompt_inputs_kernel(const __grid_
     if (!on) continue;
     float hist[K][V];
     if (owner) {
-      uint4 old[K];
-      uint4* st = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.conv) + ((size_t)row * K * p.D + c0) * sizeof(IO));
-      const size_t ss = (size_t)p.D * sizeof(IO) / 16;
+      Raw old[K];
+      Raw* st = reinterpret_cast<Raw*>(static_cast<uint8_t*>(p.conv) + ((size_t)row * K * p.D + c0) * sizeof(IO));
+      const size_t ss = (size_t)p.D / V;
       const bool res = pk.resume && pk.resume[s];
 #pragma unroll
       for (int i = 0; i < K; ++i) {
-        old[i] = res ? st[i * ss] : make_uint4(0u, 0u, 0u, 0u);
-        Vec<IO>::unpack(old[i], hist[i]);
+        old[i] = res ? st[i * ss] : Vc::zero();
+        Vc::unpack(old[i], hist[i]);
       }
       const int64_t n = end - begin;
 #pragma unroll
       for (int i = 0; i < K; ++i) {  // the last K of the rows [old | x]
-        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+        Raw u = Vc::zero();
         if (n + i >= K) {
           u = x_at(begin + n + i - K);
         } else {
@@ -157,17 +163,28 @@ __global__ void __launch_bounds__(kThreadsIn) prompt_inputs_kernel(const __grid_
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < K; ++i) Vec<IO>::unpack(x_at(ta - K + i), hist[i]);
+      for (int i = 0; i < K; ++i) Vc::unpack(x_at(ta - K + i), hist[i]);
     }
-    int64_t t = ta;
-    for (; t + U <= tb; t += U) {
-      uint4 xu[U];
+    const uint8_t* xt = x + (size_t)ta * xs;
+    uint8_t* yt = d.base + (size_t)ta * d.stride;
+    int left = (int)(tb - ta);
+    for (; left >= U; left -= U) {
+      Raw xu[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) xu[u] = x_at(t + u);
+      for (int u = 0; u < U; ++u) xu[u] = __ldg(reinterpret_cast<const Raw*>(xt + u * xs));
 #pragma unroll
-      for (int u = 0; u < U; ++u) *reinterpret_cast<uint4*>(d.base + (size_t)(t + u) * d.stride) = f.step(hist, xu[u]);
+      for (int u = 0; u < U; ++u) *reinterpret_cast<Raw*>(yt + u * d.stride) = f.step(hist, xu[u]);
+      xt += U * xs;
+      yt += U * d.stride;
     }
-    for (; t < tb; ++t) *reinterpret_cast<uint4*>(d.base + (size_t)t * d.stride) = f.step(hist, x_at(t));
+    if (left > 0) {
+      Raw xu[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) xu[u] = u < left ? __ldg(reinterpret_cast<const Raw*>(xt + u * xs)) : Vc::zero();
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u < left) *reinterpret_cast<Raw*>(yt + u * d.stride) = f.step(hist, xu[u]);
+    }
   }
 }
 
@@ -177,7 +194,10 @@ __global__ void __launch_bounds__(kThreadsIn) prompt_inputs_kernel(const __grid_
 // that the row's next entry takes, (start + count) mod cap.
 template <typename IO, int W>
 __global__ void __launch_bounds__(kThreadsIn) token_inputs_kernel(const __grid_constant__ InputsParams p) {
-  constexpr int V = Vec<IO>::n, K = W - 1;
+  using Vc = Vec<IO, kChannels>;
+  using Raw = typename Vc::raw;
+  constexpr int V = kChannels, K = W - 1;
+  constexpr int R = 4;  // rows whose loads are in flight together
   pdl_enter();
   const Packed& pk = p.pk;
   const bool steps = blockIdx.y == gridDim.y - 1;
@@ -186,71 +206,78 @@ __global__ void __launch_bounds__(kThreadsIn) token_inputs_kernel(const __grid_c
   const int r0 = (int)blockIdx.x * p.tile;
   const int r1 = r0 + p.tile < pk.n_seqs ? r0 + p.tile : pk.n_seqs;
   const int hp = p.H * p.P, gn = p.G * p.N;
+  // what the vector belongs to: v of a head, k of a group or q; and its place in a ring record
+  const int kind = c0 < hp ? 0 : c0 < hp + gn ? 1 : 2;
+  const int ck = c0 - (kind == 0 ? 0 : kind == 1 ? hp : hp + gn);
+  uint8_t* out = static_cast<uint8_t*>(kind == 0 ? p.v : kind == 1 ? p.k : p.q);
+  const size_t out_row = (size_t)(kind == 0 ? hp : gn) * sizeof(IO);
+  const int unit = kind == 0 ? p.P : p.N, of = kind == 0 ? p.H : p.G, nth = ck / unit;
+  uint8_t* ring = kind == 2 || !p.ring ? nullptr : kind == 0 ? p.ring : p.ring_k;
+  const int rec = kind == 0 ? p.rec_bytes : p.rec_k_bytes;
 
   Filter<IO, W> f;
   if (on) f.load(p, c0);
-  for (int r = r0; r < r1; ++r) {
-    const int row = seq_row(pk, r);
-    if (row < 0) continue;
-    int slot = 0;
-    if (p.ring) {
-      const int32_t word = p.counts[row];
-      const int start = word >> 16, c = word & 0xFFFF;
-      if (word < 0 || c > p.L || start >= p.cap) {
-        if (pk.status && threadIdx.x == 0) atomicOr(pk.status, kErrPointer);
-        continue;
+  const size_t ss = (size_t)p.D / V;
+  for (int rb = r0; rb < r1; rb += R) {
+    int row[R], slot[R];
+    Raw xu[R], old[R][K];
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+      row[u] = rb + u < r1 ? seq_row(pk, rb + u) : -1;
+      slot[u] = 0;
+      if (p.ring && row[u] >= 0) {
+        const int32_t word = p.counts[row[u]];
+        const int start = word >> 16, c = word & 0xFFFF;
+        if (word < 0 || c > p.L || start >= p.cap) {
+          if (pk.status && threadIdx.x == 0) atomicOr(pk.status, kErrPointer);
+          row[u] = -1;
+        }
+        slot[u] = start + c < p.cap ? start + c : start + c - p.cap;
       }
-      slot = start + c < p.cap ? start + c : start + c - p.cap;
+      if (on && row[u] >= 0) {
+        xu[u] = *reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p.x) + ((size_t)(rb + u) * p.ldx + c0) * sizeof(IO));
+        const Raw* st = reinterpret_cast<const Raw*>(static_cast<uint8_t*>(p.conv) + ((size_t)row[u] * K * p.D + c0) * sizeof(IO));
+#pragma unroll
+        for (int i = 0; i < K; ++i) old[u][i] = st[i * ss];
+      }
     }
     if (steps) {
-      for (int h = threadIdx.x; h < p.H; h += kThreadsIn) {
-        const float raw = to_float(static_cast<const IO*>(p.raw)[(size_t)r * p.ldr + h]);
-        float dt, a;
-        step_size(raw + (p.dt_bias ? p.dt_bias[h] : 0.f), p.A[h], dt, a);
-        if (p.dt) p.dt[(size_t)r * p.H + h] = dt;
-        if (p.a) p.a[(size_t)r * p.H + h] = a;
-        if (p.ring) {
-          float* e = reinterpret_cast<float*>(p.ring + (((size_t)row * p.H + h) * p.cap + slot) * p.rec_bytes +
-                                              p.P * sizeof(IO));
-          e[0] = dt;
-          e[1] = a;
+#pragma unroll
+      for (int u = 0; u < R; ++u) {
+        if (row[u] < 0) continue;
+        const int r = rb + u;
+        for (int h = threadIdx.x; h < p.H; h += kThreadsIn) {
+          const float raw = to_float(static_cast<const IO*>(p.raw)[(size_t)r * p.ldr + h]);
+          float dt, a;
+          step_size(raw + (p.dt_bias ? p.dt_bias[h] : 0.f), p.A[h], dt, a);
+          if (p.dt) p.dt[(size_t)r * p.H + h] = dt;
+          if (p.a) p.a[(size_t)r * p.H + h] = a;
+          if (p.ring) {
+            float* e = reinterpret_cast<float*>(p.ring + (((size_t)row[u] * p.H + h) * p.cap + slot[u]) * p.rec_bytes +
+                                                p.P * sizeof(IO));
+            e[0] = dt;
+            e[1] = a;
+          }
         }
       }
       continue;
     }
     if (!on) continue;
-    const uint4 xu = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x) +
-                                                     ((size_t)r * p.ldx + c0) * sizeof(IO));
-    uint4* st = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.conv) + ((size_t)row * K * p.D + c0) * sizeof(IO));
-    const size_t ss = (size_t)p.D * sizeof(IO) / 16;
-    float hist[K][V];
-    uint4 old[K];
 #pragma unroll
-    for (int i = 0; i < K; ++i) old[i] = st[i * ss];
+    for (int u = 0; u < R; ++u) {
+      if (row[u] < 0) continue;
+      float hist[K][V];
+      Raw* st = reinterpret_cast<Raw*>(static_cast<uint8_t*>(p.conv) + ((size_t)row[u] * K * p.D + c0) * sizeof(IO));
 #pragma unroll
-    for (int i = 0; i < K; ++i) {
-      Vec<IO>::unpack(old[i], hist[i]);
-      st[i * ss] = i + 1 < K ? old[i + 1 < K ? i + 1 : i] : xu;
-    }
-    const uint4 o = f.step(hist, xu);
-    const size_t at = (size_t)c0 * sizeof(IO);
-    if (c0 < hp) {
-      if (p.v) *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.v) + (size_t)r * hp * sizeof(IO) + at) = o;
-      if (p.ring) {
-        const int h = c0 / p.P;
-        *reinterpret_cast<uint4*>(p.ring + (((size_t)row * p.H + h) * p.cap + slot) * p.rec_bytes +
-                                  (size_t)(c0 - h * p.P) * sizeof(IO)) = o;
+      for (int i = 0; i < K; ++i) {
+        Vc::unpack(old[u][i], hist[i]);
+        st[i * ss] = i + 1 < K ? old[u][i + 1 < K ? i + 1 : i] : xu[u];
       }
-    } else if (c0 < hp + gn) {
-      const int ck = c0 - hp;
-      if (p.k) *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.k) + ((size_t)r * gn + ck) * sizeof(IO)) = o;
-      if (p.ring) {
-        const int g = ck / p.N;
-        *reinterpret_cast<uint4*>(p.ring_k + (((size_t)row * p.G + g) * p.cap + slot) * p.rec_k_bytes +
-                                  (size_t)(ck - g * p.N) * sizeof(IO)) = o;
-      }
-    } else {
-      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.q) + ((size_t)r * gn + c0 - hp - gn) * sizeof(IO)) = o;
+      const Raw o = f.step(hist, xu[u]);
+      if (out) *reinterpret_cast<Raw*>(out + (size_t)(rb + u) * out_row + (size_t)ck * sizeof(IO)) = o;
+      if (ring)
+        *reinterpret_cast<Raw*>(ring + (((size_t)row[u] * of + nth) * p.cap + slot[u]) * rec +
+                                (size_t)(ck - nth * unit) * sizeof(IO)) = o;
     }
   }
 }
@@ -275,17 +302,18 @@ cudaError_t token_io(const InputsParams& p, dim3 grid, cudaStream_t s) {
     default: return cudaErrorInvalidValue;
   }
 }
-int channel_blocks(const InputsParams& p, int io) {
-  const int v = io == 1 ? 8 : 4;
-  return (p.D / v + kThreadsIn - 1) / kThreadsIn;
-}
+int channel_blocks(const InputsParams& p) { return (p.D / kChannels + kThreadsIn - 1) / kThreadsIn; }
 
 }  // namespace
 
 cudaError_t launch_prompt_inputs(const InputsParams& in, int io, int num_sms, cudaStream_t s) {
   InputsParams p = in;
-  const int cb = channel_blocks(p, io);
-  p.tile = 32;
+  const int cb = channel_blocks(p);
+  // A block starts with a search and the rows before its tile: long tiles, but enough blocks
+  // to fill the SMs, and few sequences behind one another in a tile where they are short.
+  p.tile = 64;
+  while (p.tile > 8 && (p.pk.tokens / p.tile * cb < 8 * num_sms || p.pk.tokens < (int64_t)p.tile * p.pk.n_seqs / 2))
+    p.tile /= 2;
   const int64_t tiles = p.pk.tokens > 0 ? (p.pk.tokens + p.tile - 1) / p.tile : 1;
   const dim3 grid((unsigned)tiles, cb + 1);
   return io == 1 ? prompt_io<__nv_bfloat16>(p, grid, s) : prompt_io<float>(p, grid, s);
@@ -293,8 +321,9 @@ cudaError_t launch_prompt_inputs(const InputsParams& in, int io, int num_sms, cu
 
 cudaError_t launch_token_inputs(const InputsParams& in, int io, int num_sms, cudaStream_t s) {
   InputsParams p = in;
-  const int cb = channel_blocks(p, io);
-  p.tile = 1;
+  const int cb = channel_blocks(p);
+  p.tile = 4;  // rows of a block: the filter is loaded once for them
+  while (p.tile > 1 && (int64_t)p.pk.n_seqs * cb < (int64_t)4 * num_sms * p.tile) p.tile /= 2;
   const dim3 grid((unsigned)((p.pk.n_seqs + p.tile - 1) / p.tile), cb + 1);
   return io == 1 ? token_io<__nv_bfloat16>(p, grid, s) : token_io<float>(p, grid, s);
 }

@@ -8,46 +8,47 @@ namespace replay {
 
 namespace {
 
-template <typename IO>
-__device__ __forceinline__ float gate(float z) {
-  if constexpr (sizeof(IO) == 2) return __fdividef(z, 1.f + __expf(-z));
-  return z / (1.f + expf(-z));
-}
-
-// V consecutive values of y (FP32 or io) as floats
-template <typename Y, int V>
-__device__ __forceinline__ void load_y(const void* y, size_t i, float* f) {
-  constexpr int n = Vec<Y>::n;
-#pragma unroll
-  for (int j = 0; j < V; j += n)
-    Vec<Y>::unpack(*reinterpret_cast<const uint4*>(static_cast<const Y*>(y) + i + j), f + j);
-}
-
-// u of the V elements from column c of row r
+// The inputs of the V elements from column c of row r
 template <typename IO, typename Y>
-__device__ __forceinline__ void gated(const NormParams& p, int64_t r, int c, float* u) {
-  constexpr int V = Vec<IO>::n;
-  const size_t at = (size_t)r * p.H * p.P + c;
-  float z[V];
-  load_y<Y, V>(p.y, at, u);
-  Vec<IO>::unpack(*reinterpret_cast<const uint4*>(static_cast<const IO*>(p.z) + (size_t)r * p.ldz + c), z);
-  if (p.v) {
-    float v[V];
-    Vec<IO>::unpack(*reinterpret_cast<const uint4*>(static_cast<const IO*>(p.v) + at), v);
-    const float skip = p.D[c / p.P];  // P is a multiple of 8: one head per vector
+struct NormIn {
+  static constexpr int V = Vec<IO>::n, YN = V / Vec<Y>::n;
+  uint4 y[YN], z, v;
+  __device__ __forceinline__ void load(const NormParams& p, int64_t r, int c) {
+    const size_t at = (size_t)r * p.H * p.P + c;
 #pragma unroll
-    for (int j = 0; j < V; ++j) u[j] = fmaf(skip, v[j], u[j]);
+    for (int j = 0; j < YN; ++j)
+      y[j] = *reinterpret_cast<const uint4*>(static_cast<const Y*>(p.y) + at + j * Vec<Y>::n);
+    z = *reinterpret_cast<const uint4*>(static_cast<const IO*>(p.z) + (size_t)r * p.ldz + c);
+    if (p.v) v = *reinterpret_cast<const uint4*>(static_cast<const IO*>(p.v) + at);
   }
+  // u
+  __device__ __forceinline__ void gated(const NormParams& p, int c, float* u) const {
+    float zf[V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) u[j] *= gate<IO>(z[j]);
-}
+    for (int j = 0; j < YN; ++j) Vec<Y>::unpack(y[j], u + j * Vec<Y>::n);
+    Vec<IO>::unpack(z, zf);
+    if (p.v) {
+      float vf[V];
+      Vec<IO>::unpack(v, vf);
+      const float skip = p.D[__umulhi((uint32_t)c >> 3, p.head_magic) + (p.P == 8 ? (uint32_t)c >> 3 : 0u)];  // D of the head c / P
+#pragma unroll
+      for (int j = 0; j < V; ++j) u[j] = fmaf(skip, vf[j], u[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) u[j] *= silu<IO>(zf[j]);
+  }
+};
 
 template <typename IO>
 __device__ __forceinline__ void scale_store(const NormParams& p, int64_t r, int c, const float* u, float inv) {
   constexpr int V = Vec<IO>::n;
   float o[V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) o[j] = u[j] * inv * p.weight[c + j];
+  for (int j = 0; j < V; j += 4) {
+    const float4 w = *reinterpret_cast<const float4*>(p.weight + c + j);
+    o[j] = u[j] * inv * w.x, o[j + 1] = u[j + 1] * inv * w.y;
+    o[j + 2] = u[j + 2] * inv * w.z, o[j + 3] = u[j + 3] * inv * w.w;
+  }
   *reinterpret_cast<uint4*>(static_cast<IO*>(p.out) + (size_t)r * p.H * p.P + c) = Vec<IO>::pack(o);
 }
 
@@ -73,18 +74,22 @@ __global__ void __launch_bounds__(T > 256 ? T : 256) gated_norm_kernel(const __g
   float u[NV][V];
   float sum = 0.f;
   if (on) {
+    NormIn<IO, Y> in[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if ((i * T + tid) * V < width) in[i].load(p, r, c0 + (i * T + tid) * V);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * T + tid) * V;
-      if (c < width) {
-        gated<IO, Y>(p, r, c0 + c, u[i]);
+      if ((i * T + tid) * V < width) {
+        in[i].gated(p, c0 + (i * T + tid) * V, u[i]);
 #pragma unroll
         for (int j = 0; j < V; ++j) sum = fmaf(u[i][j], u[i][j], sum);
       }
     }
     for (int c = (NV * T + tid) * V; c < width; c += T * V) {
       float x[V];
-      gated<IO, Y>(p, r, c0 + c, x);
+      in[0].load(p, r, c0 + c);
+      in[0].gated(p, c0 + c, x);
 #pragma unroll
       for (int j = 0; j < V; ++j) sum = fmaf(x[j], x[j], sum);
     }
@@ -107,7 +112,9 @@ __global__ void __launch_bounds__(T > 256 ? T : 256) gated_norm_kernel(const __g
   }
   for (int c = (NV * T + tid) * V; c < width; c += T * V) {
     float x[V];
-    gated<IO, Y>(p, r, c0 + c, x);
+    NormIn<IO, Y> in;
+    in.load(p, r, c0 + c);
+    in.gated(p, c0 + c, x);
     scale_store<IO>(p, r, c0 + c, x, inv);
   }
 }
@@ -126,7 +133,9 @@ cudaError_t norm_io(const NormParams& p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_gated_norm(const NormParams& p, int io, int y_io, int num_sms, cudaStream_t s) {
+cudaError_t launch_gated_norm(const NormParams& in, int io, int y_io, int num_sms, cudaStream_t s) {
+  NormParams p = in;
+  p.head_magic = p.P == 8 ? 0u : (uint32_t)(((1ull << 32) + p.P / 8 - 1) / (p.P / 8));
   if (io == 1) return y_io == 1 ? norm_io<__nv_bfloat16, __nv_bfloat16>(p, s) : norm_io<__nv_bfloat16, float>(p, s);
   return norm_io<float, float>(p, s);
 }

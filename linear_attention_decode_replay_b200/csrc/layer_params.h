@@ -68,6 +68,7 @@ struct NormParams {
   const float *D, *weight;
   float eps;
   void* out;  // [rows][H * P] io
+  uint32_t head_magic;  // 2^32 / (P / 8) rounded up: the head of column c is (c / 8) head_magic / 2^32
 };
 
 // io: 0 = FP32, 1 = BF16
