@@ -41,6 +41,7 @@ half of the pointer words is current, so capture two windows when L is odd:
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -89,6 +90,13 @@ class Config:
     @property
     def io_dtype(self) -> torch.dtype:
         return torch.bfloat16 if self.io == "bf16" else torch.float32
+
+    @functools.cached_property
+    def _layer(self):
+        """What the calls around the step need of it: the C config by reference, the io
+        dtype, the channels and the shapes of one token's q (k), v and dt (a)."""
+        H, G, P, N = self.heads, self.groups, self.P, self.N
+        return ctypes.byref(self.c()), self.io_dtype, H * P + 2 * G * N, (G, N), (H, P), (H,)
 
 
 def ring_capacity(cfg: Config) -> int:
@@ -171,83 +179,101 @@ def _ptr(t, shape=None, dtype=None, name="tensor"):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _rows(t, n, width, dtype, name):
-    """Pointer and row stride (elements) of a 2-D tensor whose rows may lie apart."""
+# The calls around the step are short beside what Python spends on their arguments, so their
+# checks are one expression a tensor, and say what is wrong only where something is.
+def _arg(t, shape, dtype, name, dev):
+    """Address of a dense tensor of this shape and dtype on CUDA device `dev` (None: none)."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _ptr(t, shape, dtype, name)
+    raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+
+
+def _rows(t, n, width, dtype, name, dev):
+    """Address and row stride (elements) of a 2-D tensor whose rows may lie apart."""
+    try:
+        if t.dtype is dtype and t.shape == (n, width) and t.get_device() == dev:
+            row, col = t.stride()
+            if col == 1 or width == 1:  # the stride of a single row says nothing
+                return t.data_ptr(), row if n > 1 else (width + 7) // 8 * 8
+            raise ValueError(f"{name} must have contiguous rows")
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must have shape {(n, width)}, got {tuple(t.shape)}")
+
+
+def _device_of(t, name):
+    """Index of the CUDA device that a call's tensors must be on: its first tensor's."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != width:
-        raise ValueError(f"{name} must have shape {(n, width)}, got {tuple(t.shape)}")
-    if width > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    # the stride of a single row says nothing
-    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if n > 1 else (width + 7) // 8 * 8
+    return t.get_device()
 
 
-def _same_device(first, *others):
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors are on different devices: {first.device} and {t.device}")
-    return first.device
+def _on(dev, stream, body):
+    """body(raw stream) with device `dev` current and `stream` (None: its current one) the
+    stream of the allocations in it, so that none is handed to another stream's work early."""
+    if stream is None and torch._C._cuda_getDevice() == dev:
+        return body(torch._C._cuda_getCurrentRawStream(dev))
+    with torch.cuda.device(dev):
+        if stream is None:
+            return body(torch._C._cuda_getCurrentRawStream(dev))
+        with torch.cuda.stream(stream):
+            return body(stream.cuda_stream)
 
 
-class _On:
-    """Makes `device` current, and `stream` (None: the device's current one) the stream of
-    the allocations inside, so that scratch is not handed to another stream's work early."""
-
-    def __init__(self, device, stream):
-        self._dev = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-        self._stream = None if stream is None else torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self._dev is not None:
-            self._dev.__enter__()
-        if self._stream is not None:
-            self._stream.__enter__()
-        return _stream(None)
-
-    def __exit__(self, *exc):
-        if self._stream is not None:
-            self._stream.__exit__(*exc)
-        if self._dev is not None:
-            self._dev.__exit__(*exc)
+def _width(cfg, w):
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError(f"w must be a tensor of shape (width, {cfg._layer[2]})")
+    return w.shape[0]
 
 
-def _channels(cfg):
-    return cfg.heads * cfg.P + 2 * cfg.groups * cfg.N
+def _filter_args(cfg, conv, w, A, bias, dt_bias, dev):
+    """width, and the addresses of w, bias, dt_bias, A and conv."""
+    _, t, D, _, _, hs = cfg._layer
+    width, f32 = _width(cfg, w), torch.float32
+    return (width, _arg(w, (width, D), f32, "w", dev), _arg(bias, (D,), f32, "bias", dev),
+            _arg(dt_bias, hs, f32, "dt_bias", dev), _arg(A, hs, f32, "A", dev),
+            _arg(conv, (cfg.batch, width - 1, D), t, "conv", dev))
 
 
-def _filter_args(cfg, conv, w, A, bias, dt_bias):
-    """width and the pointers w, bias, dt_bias, A, conv of the convolution's arguments."""
-    D, f32 = _channels(cfg), torch.float32
-    if w.dim() != 2:
-        raise ValueError(f"w must have shape (width, {D}), got {tuple(w.shape)}")
-    width = w.shape[0]
-    return (width, _ptr(w, (width, D), f32, "w"), _ptr(bias, (D,), f32, "bias"),
-            _ptr(dt_bias, (cfg.heads,), f32, "dt_bias"), _ptr(A, (cfg.heads,), f32, "A"),
-            _ptr(conv, (cfg.batch, width - 1, D), cfg.io_dtype, "conv"))
-
-
-def _packed_args(cu_seqlens, seqs, resume):
-    """n_seqs and the pointers cu_seqlens, seqs, resume."""
+def _n_seqs(cu_seqlens):
     if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must be a tensor of n_seqs + 1 offsets")
-    n = cu_seqlens.shape[0] - 1
-    return (n, _ptr(cu_seqlens, (n + 1,), torch.int32, "cu_seqlens"), _ptr(seqs, (n,), torch.int32, "seqs"),
-            _ptr(resume, (n,), torch.uint8, "resume"))
+    return cu_seqlens.shape[0] - 1
 
 
-def _alloc_inputs(cfg, n, device, out):
-    """q, k, v, dt, a of n tokens: `out` checked, or new tensors."""
-    t, f32 = cfg.io_dtype, torch.float32
-    shapes = (((n, cfg.groups, cfg.N), t), ((n, cfg.groups, cfg.N), t), ((n, cfg.heads, cfg.P), t),
-              ((n, cfg.heads), f32), ((n, cfg.heads), f32))
+def _packed_args(cu_seqlens, seqs, resume, dev):
+    """n_seqs, and the addresses of cu_seqlens, seqs and resume."""
+    n = _n_seqs(cu_seqlens)
+    return (n, _arg(cu_seqlens, (n + 1,), torch.int32, "cu_seqlens", dev), _arg(seqs, (n,), torch.int32, "seqs", dev),
+            _arg(resume, (n,), torch.uint8, "resume", dev))
+
+
+def _input_outs(cfg, n, like, out, dev):
+    """q, k, v, dt, a of n tokens, `out` checked or new tensors, and their addresses."""
+    _, t, _, qs, vs, hs = cfg._layer
     if out is None:
-        out = tuple(torch.empty(s, device=device, dtype=d) for s, d in shapes)
-    return out, [_ptr(o, s, d, name) for o, (s, d), name in zip(out, shapes, ("q", "k", "v", "dt", "a"), strict=True)]
+        q, k, v = like.new_empty((n, *qs)), like.new_empty((n, *qs)), like.new_empty((n, *vs))
+        dt = like.new_empty((n, *hs), dtype=torch.float32)
+        a = like.new_empty((n, *hs), dtype=torch.float32)
+        return (q, k, v, dt, a), (q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(), a.data_ptr())
+    q, k, v, dt, a = out
+    f32 = torch.float32
+    return out, (_arg(q, (n, *qs), t, "q", dev), _arg(k, (n, *qs), t, "k", dev), _arg(v, (n, *vs), t, "v", dev),
+                 _arg(dt, (n, *hs), f32, "dt", dev), _arg(a, (n, *hs), f32, "a", dev))
 
 
 class Replay:
@@ -382,40 +408,43 @@ class Replay:
     def append_inputs(self, conv, x, raw, w, A, bias=None, dt_bias=None, q=None, v=None, stream=None):
         """token_inputs() of every sequence, its entry written straight into the ring; returns
         q for step_resident(), which must come next, and v (for gated_norm's skip term)."""
-        cfg, t = self.cfg, self.cfg.io_dtype
-        B, H, G, P, N = cfg.batch, cfg.heads, cfg.groups, cfg.P, cfg.N
-        width, *ptrs, cp = _filter_args(cfg, conv, w, A, bias, dt_bias)
-        xp, ldx = _rows(x, B, _channels(cfg), t, "x")
-        rp, ldr = _rows(raw, B, H, t, "raw")
-        with _On(_same_device(self.buffers["S0"], conv, x, raw, w, A, bias, dt_bias, q, v), stream) as st:
-            if q is None:
-                q = torch.empty(B, G, N, device=x.device, dtype=t)
-            if v is None:
-                v = torch.empty(B, H, P, device=x.device, dtype=t)
-            check(self._lib.replay_append_inputs(self._ctx, width, xp, ldx, rp, ldr, *ptrs, cp,
-                                                 _ptr(q, (B, G, N), t, "q"), _ptr(v, (B, H, P), t, "v"), st),
+        cfg, B = self.cfg, self.cfg.batch
+        _, t, D, qs, vs, _ = cfg._layer
+        dev = self.buffers["S0"].get_device()
+        width, *ptrs = _filter_args(cfg, conv, w, A, bias, dt_bias, dev)
+        xp, ldx = _rows(x, B, D, t, "x", dev)
+        rp, ldr = _rows(raw, B, cfg.heads, t, "raw", dev)
+
+        def body(st):
+            q1 = x.new_empty((B, *qs)) if q is None else q
+            v1 = x.new_empty((B, *vs)) if v is None else v
+            check(self._lib.replay_append_inputs(self._ctx, width, xp, ldx, rp, ldr, *ptrs,
+                                                 _arg(q1, (B, *qs), t, "q", dev), _arg(v1, (B, *vs), t, "v", dev), st),
                   "replay_append_inputs")
-        return q, v
+            return q1, v1
+
+        return _on(dev, stream, body)
 
     def prefill(self, q, k, v, dt, a, cu_seqlens, seqs=None, resume=None, y=None, max_len=0, scratch=None, stream=None):
         """prompt_scan() into the layer: packed prompts become the states that step() decodes
         on from. Sequence i is the layer's sequence seqs[i]; where resume[i], it continues
         from that sequence's checkpoint and buffered entries. Returns y [T][H][P] io."""
-        n, cu, sp, rp = _packed_args(cu_seqlens, seqs, resume)
-        T = q.shape[0]
-        ptrs, y_shape = _scan_args(self.cfg, T, q, k, v, dt, a)
-        with _On(_same_device(self.buffers["S0"], q, k, v, dt, a, cu_seqlens, seqs, resume, y, scratch), stream) as st:
-            if y is None:
-                y = torch.empty(y_shape, device=q.device, dtype=self.cfg.io_dtype)
+        dev, T = self.buffers["S0"].get_device(), q.shape[0]
+        n, cu, sp, rp = _packed_args(cu_seqlens, seqs, resume, dev)
+        ptrs, y_shape = _scan_args(self.cfg, T, q, k, v, dt, a, dev)
+
+        def body(st):
+            y1 = v.new_empty(y_shape) if y is None else y
             need = self._lib.replay_prefill_scratch(self._ctx, T, n, max_len)
             check(min(need, 0), "replay_prefill_scratch")
-            if scratch is None:
-                scratch = torch.empty(need, device=q.device, dtype=torch.uint8)
+            sc = v.new_empty(need, dtype=torch.uint8) if scratch is None else scratch
             check(self._lib.replay_prefill(self._ctx, T, *ptrs, cu, sp, rp, n, max_len,
-                                           _ptr(y, y_shape, self.cfg.io_dtype, "y"),
-                                           _ptr(scratch, None, torch.uint8, "scratch"), scratch.numel(), st),
+                                           _arg(y1, y_shape, v.dtype, "y", dev),
+                                           _arg(sc, sc.shape, torch.uint8, "scratch", dev), sc.numel(), st),
                   "replay_prefill")
-        return y
+            return y1
+
+        return _on(dev, stream, body)
 
     def rollback(self, n_keep, stream=None):
         """Keep n_keep[b] (int32 [B] on the device) of the pending verify's positions."""
@@ -522,43 +551,51 @@ def prompt_inputs(cfg: Config, conv, x, raw, w, A, cu_seqlens, bias=None, dt_bia
     always updated. w [width][D], bias [D], dt_bias, A [H] are FP32; cu_seqlens int32
     [n + 1], seqs int32 [n] (rows; None = 0..n-1), resume uint8 [n] (None = none).
     Returns (q, k, v, dt, a)."""
-    width, *ptrs, cp = _filter_args(cfg, conv, w, A, bias, dt_bias)
-    n, cu, sp, rp = _packed_args(cu_seqlens, seqs, resume)
-    T = x.shape[0]
-    xp, ldx = _rows(x, T, _channels(cfg), cfg.io_dtype, "x")
-    rawp, ldr = _rows(raw, T, cfg.heads, cfg.io_dtype, "raw")
-    device = _same_device(x, conv, raw, w, A, cu_seqlens, bias, dt_bias, seqs, resume, status, *(out or ()))
-    with _On(device, stream) as st:
-        out, outs = _alloc_inputs(cfg, T, device, out)
-        check(load().replay_prompt_inputs(ctypes.byref(cfg.c()), width, T, xp, ldx, rawp, ldr, *ptrs, cu, sp, rp, n, cp,
-                                          *outs, _ptr(status, (1,), torch.int32, "status"), st),
-              "replay_prompt_inputs")
-    return out
+    dev, T = _device_of(x, "x"), x.shape[0]
+    c, t, D, *_ = cfg._layer
+    width, wp, bp, dbp, Ap, cp = _filter_args(cfg, conv, w, A, bias, dt_bias, dev)
+    n, cu, sp, rp = _packed_args(cu_seqlens, seqs, resume, dev)
+    xp, ldx = _rows(x, T, D, t, "x", dev)
+    rawp, ldr = _rows(raw, T, cfg.heads, t, "raw", dev)
+    stp = _arg(status, (1,), torch.int32, "status", dev)
+
+    def body(st):
+        o, ptrs = _input_outs(cfg, T, x, out, dev)
+        check(load().replay_prompt_inputs(c, width, T, xp, ldx, rawp, ldr, wp, bp, dbp, Ap, cu, sp, rp, n, cp, *ptrs, stp,
+                                          st), "replay_prompt_inputs")
+        return o
+
+    return _on(dev, stream, body)
 
 
 def token_inputs(cfg: Config, conv, x, raw, w, A, bias=None, dt_bias=None, seqs=None, out=None, status=None,
                  stream=None):
     """prompt_inputs() for one decode token of each of n rows, from and to the state: row i
     of x belongs to row seqs[i] of conv (None = i; a negative id is padding)."""
-    width, *ptrs, cp = _filter_args(cfg, conv, w, A, bias, dt_bias)
-    n = x.shape[0]
-    xp, ldx = _rows(x, n, _channels(cfg), cfg.io_dtype, "x")
-    rawp, ldr = _rows(raw, n, cfg.heads, cfg.io_dtype, "raw")
-    device = _same_device(x, conv, raw, w, A, bias, dt_bias, seqs, status, *(out or ()))
-    with _On(device, stream) as st:
-        out, outs = _alloc_inputs(cfg, n, device, out)
-        check(load().replay_token_inputs(ctypes.byref(cfg.c()), width, n, xp, ldx, rawp, ldr, *ptrs,
-                                         _ptr(seqs, (n,), torch.int32, "seqs"), cp, *outs,
-                                         _ptr(status, (1,), torch.int32, "status"), st), "replay_token_inputs")
-    return out
+    _width(cfg, w)
+    dev, n = _device_of(x, "x"), x.shape[0]
+    c, t, D, *_ = cfg._layer
+    width, wp, bp, dbp, Ap, cp = _filter_args(cfg, conv, w, A, bias, dt_bias, dev)
+    xp, ldx = _rows(x, n, D, t, "x", dev)
+    rawp, ldr = _rows(raw, n, cfg.heads, t, "raw", dev)
+    sp = _arg(seqs, (n,), torch.int32, "seqs", dev)
+    stp = _arg(status, (1,), torch.int32, "status", dev)
+
+    def body(st):
+        o, ptrs = _input_outs(cfg, n, x, out, dev)
+        check(load().replay_token_inputs(c, width, n, xp, ldx, rawp, ldr, wp, bp, dbp, Ap, sp, cp, *ptrs, stp, st),
+              "replay_token_inputs")
+        return o
+
+    return _on(dev, stream, body)
 
 
-def _scan_args(cfg, T, q, k, v, dt, a):
-    """Pointers q, k, v, dt, a of T packed tokens, and the shape of y."""
-    t, f32 = cfg.io_dtype, torch.float32
-    kn, hp = (T, cfg.groups, cfg.N), (T, cfg.heads, cfg.P)
-    return (_ptr(q, kn, t, "q"), _ptr(k, kn, t, "k"), _ptr(v, hp, t, "v"), _ptr(dt, hp[:2], f32, "dt"),
-            _ptr(a, hp[:2], f32, "a")), hp
+def _scan_args(cfg, T, q, k, v, dt, a, dev):
+    """Addresses of q, k, v, dt, a of T packed tokens, and the shape of y."""
+    _, t, _, qs, vs, hs = cfg._layer
+    kn, hp, h, f32 = (T, *qs), (T, *vs), (T, *hs), torch.float32
+    return (_arg(q, kn, t, "q", dev), _arg(k, kn, t, "k", dev), _arg(v, hp, t, "v", dev), _arg(dt, h, f32, "dt", dev),
+            _arg(a, h, f32, "a", dev)), hp
 
 
 def prompt_scan(cfg: Config, S, q, k, v, dt, a, cu_seqlens, seqs=None, resume=None, y=None, max_len=0, scratch=None,
@@ -568,25 +605,29 @@ def prompt_scan(cfg: Config, S, q, k, v, dt, a, cu_seqlens, seqs=None, resume=No
     states go back to S. q, k [T][G][N], v [T][H][P] (io), dt, a [T][H] (FP32), cu_seqlens
     int32 [n + 1], seqs int32 [n], resume uint8 [n]. max_len, if known, steers how the work
     is split. Returns y [T][H][P] (io)."""
-    n, cu, sp, rp = _packed_args(cu_seqlens, seqs, resume)
-    T = q.shape[0]
-    ptrs, y_shape = _scan_args(cfg, T, q, k, v, dt, a)
-    Sp = _ptr(S, (cfg.batch, cfg.heads, cfg.P, cfg.N), torch.float32, "S")
-    device = _same_device(q, S, k, v, dt, a, cu_seqlens, seqs, resume, y, scratch, status)
-    lib, c = load(), cfg.c()
-    with _On(device, stream) as st:
-        if y is None:
-            y = torch.empty(y_shape, device=device, dtype=cfg.io_dtype)
-        if scratch is None:
-            need = lib.replay_prompt_scan_scratch(ctypes.byref(c), T, n, max_len)
+    _n_seqs(cu_seqlens)
+    dev, T = _device_of(q, "q"), q.shape[0]
+    c = cfg._layer[0]
+    n, cu, sp, rp = _packed_args(cu_seqlens, seqs, resume, dev)
+    ptrs, y_shape = _scan_args(cfg, T, q, k, v, dt, a, dev)
+    Sp = _arg(S, (cfg.batch, cfg.heads, cfg.P, cfg.N), torch.float32, "S", dev)
+    stp = _arg(status, (1,), torch.int32, "status", dev)
+    lib = load()
+
+    def body(st):
+        y1 = v.new_empty(y_shape) if y is None else y
+        sc = scratch
+        if sc is None:
+            need = lib.replay_prompt_scan_scratch(c, T, n, max_len)
             check(min(need, 0), "replay_prompt_scan_scratch")
             if need:
-                scratch = torch.empty(need, device=device, dtype=torch.uint8)
-        check(lib.replay_prompt_scan(ctypes.byref(c), T, *ptrs, cu, sp, rp, n, max_len, Sp,
-                                     _ptr(y, y_shape, cfg.io_dtype, "y"), _ptr(scratch, None, torch.uint8, "scratch"),
-                                     0 if scratch is None else scratch.numel(),
-                                     _ptr(status, (1,), torch.int32, "status"), st), "replay_prompt_scan")
-    return y
+                sc = v.new_empty(need, dtype=torch.uint8)
+        scp, sb = (None, 0) if sc is None else (_arg(sc, sc.shape, torch.uint8, "scratch", dev), sc.numel())
+        check(lib.replay_prompt_scan(c, T, *ptrs, cu, sp, rp, n, max_len, Sp, _arg(y1, y_shape, v.dtype, "y", dev), scp, sb,
+                                     stp, st), "replay_prompt_scan")
+        return y1
+
+    return _on(dev, stream, body)
 
 
 def gated_norm(cfg: Config, y, z, weight, v=None, D=None, norm_groups=1, eps=1e-5, out=None, stream=None):
@@ -594,18 +635,20 @@ def gated_norm(cfg: Config, y, z, weight, v=None, D=None, norm_groups=1, eps=1e-
     sqrt(mean(u^2) + eps), the mean over each of norm_groups equal parts of a row. y
     [T][H][P] (FP32 or io), z [T][H*P] (io; rows may be slices of wider ones), weight
     [H*P] FP32; v [T][H][P] (io) and D [H] (FP32) for the skip term. Returns [T][H*P] io."""
-    T, hp, t = y.shape[0], (y.shape[0], cfg.heads, cfg.P), cfg.io_dtype
-    width = cfg.heads * cfg.P
-    y_type = _abi.REPLAY_F32 if y.dtype == torch.float32 else _abi.REPLAY_BF16
-    if y.dtype not in (torch.float32, t):
+    c, t, _, _, vs, hs = cfg._layer
+    if y.dtype is not torch.float32 and y.dtype is not t:
         raise ValueError(f"y must have dtype {torch.float32} or {t}, got {y.dtype}")
-    zp, ldz = _rows(z, T, width, t, "z")
-    device = _same_device(y, z, weight, v, D, out)
-    with _On(device, stream) as st:
-        if out is None:
-            out = torch.empty(T, width, device=device, dtype=t)
-        check(load().replay_gated_norm(ctypes.byref(cfg.c()), T, _ptr(y, hp, y.dtype, "y"), y_type, zp, ldz,
-                                       _ptr(v, hp, t, "v"), _ptr(D, (cfg.heads,), torch.float32, "D"),
-                                       _ptr(weight, (width,), torch.float32, "weight"), norm_groups, eps,
-                                       _ptr(out, (T, width), t, "out"), st), "replay_gated_norm")
-    return out
+    dev, T = _device_of(z, "z"), y.shape[0]
+    width, hp = cfg.heads * cfg.P, (T, *vs)
+    y_type = _abi.REPLAY_F32 if y.dtype is torch.float32 else _abi.REPLAY_BF16
+    yp, wp = _arg(y, hp, y.dtype, "y", dev), _arg(weight, (width,), torch.float32, "weight", dev)
+    zp, ldz = _rows(z, T, width, t, "z", dev)
+    vp, Dp = _arg(v, hp, t, "v", dev), _arg(D, hs, torch.float32, "D", dev)
+
+    def body(st):
+        o = z.new_empty((T, width)) if out is None else out
+        check(load().replay_gated_norm(c, T, yp, y_type, zp, ldz, vp, Dp, wp, norm_groups, eps,
+                                       _arg(o, (T, width), t, "out", dev), st), "replay_gated_norm")
+        return o
+
+    return _on(dev, stream, body)

@@ -56,6 +56,7 @@ int inputs_params(InputsParams* p, const replay_config& c, int32_t width, int64_
   if (width < 2 || width > kMaxWidth) return REPLAY_EINVAL;
   const int64_t D = (int64_t)c.heads * c.P + 2 * (int64_t)c.groups * c.N;
   if (D > INT32_MAX / 8) return REPLAY_EINVAL;
+  if ((rows / 8 + 1) * (D / 512 + 2) > INT32_MAX) return REPLAY_EINVAL;  // blocks of one launch
   if (!w || !A || !conv || (rows > 0 && (!x || !raw))) return REPLAY_EINVAL;
   if (ldx < D || ldr < c.heads) return REPLAY_EINVAL;
   const int s = io_bytes(c);

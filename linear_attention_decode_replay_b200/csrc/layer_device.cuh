@@ -65,7 +65,8 @@ struct Vec<__nv_bfloat16, 4> {
   __device__ __forceinline__ static uint2 zero() { return make_uint2(0u, 0u); }
 };
 // x sigmoid(x). For BF16 results the hardware's exponential and reciprocal, each within a
-// few units of 2^-23 (the result's own rounding is 2^-9); for FP32 results the accurate ones.
+// few units of 2^-23 (the result's own rounding is 2^-9); for FP32 results the accurate
+// exponential and a division within 2 steps (results under 2^-120 may become 0).
 template <typename IO>
 __device__ __forceinline__ float silu(float x) {
   if constexpr (sizeof(IO) == 2) {
@@ -74,7 +75,7 @@ __device__ __forceinline__ float silu(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
     return x * r;
   }
-  return x / (1.f + expf(-x));
+  return __fdividef(x, 1.f + expf(-x));
 }
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }

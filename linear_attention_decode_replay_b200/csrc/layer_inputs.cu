@@ -73,23 +73,26 @@ __device__ __forceinline__ Dest dest_of(const InputsParams& p, int c0) {
 }  // namespace
 
 // Packed prompts. A block takes a tile of tokens and kThreadsIn vectors of channels (the
-// last row of blocks: the tile's step sizes); a thread walks its tokens with the filter's
+// last one of a tile: its step sizes); a thread walks its tokens with the filter's
 // rows in registers. The tile that holds a sequence's first token also takes the
 // width - 2 tokens after it, wherever they lie, and writes the sequence's new state, so
 // that the thread that writes a state element is the only one that reads it.
 template <typename IO, int W>
-__global__ void __launch_bounds__(kThreadsIn) prompt_inputs_kernel(const __grid_constant__ InputsParams p) {
+__global__ void __launch_bounds__(kThreadsIn, 6) prompt_inputs_kernel(const __grid_constant__ InputsParams p) {
   using Vc = Vec<IO, kChannels>;
   using Raw = typename Vc::raw;
   constexpr int V = kChannels, K = W - 1;
-  constexpr int U = 8;  // tokens whose loads are in flight together
+  constexpr int U = 4;  // tokens whose loads are in flight together
   pdl_enter();
   const Packed& pk = p.pk;
-  const int64_t t0 = (int64_t)blockIdx.x * p.tile;
-  const bool last = blockIdx.x == gridDim.x - 1;
+  // blocks of the same tokens are neighbours, so that the rows are read as a whole
+  const int cols = p.col_blocks;
+  const int tile = blockIdx.x / cols, col = blockIdx.x % cols;
+  const int64_t t0 = (int64_t)tile * p.tile;
+  const bool last = blockIdx.x >= gridDim.x - cols;
   const int64_t t1 = last ? pk.tokens : t0 + p.tile;
-  const bool steps = blockIdx.y == gridDim.y - 1;
-  const int c0 = ((int)blockIdx.y * kThreadsIn + (int)threadIdx.x) * V;
+  const bool steps = col == cols - 1;
+  const int c0 = (col * kThreadsIn + (int)threadIdx.x) * V;
   const bool on = !steps && c0 < p.D;
 
   Filter<IO, W> f;
@@ -168,28 +171,35 @@ __global__ void __launch_bounds__(kThreadsIn) prompt_inputs_kernel(const __grid_
     const uint8_t* xt = x + (size_t)ta * xs;
     uint8_t* yt = d.base + (size_t)ta * d.stride;
     int left = (int)(tb - ta);
-    for (; left >= U; left -= U) {
-      Raw xu[U];
+    // two groups of U tokens: one in flight while the other is computed
+    Raw xu[2][U];
+    auto fetch = [&](Raw* g) {  // the next U tokens from xt on, as far as there are any
 #pragma unroll
-      for (int u = 0; u < U; ++u) xu[u] = __ldg(reinterpret_cast<const Raw*>(xt + u * xs));
-#pragma unroll
-      for (int u = 0; u < U; ++u) *reinterpret_cast<Raw*>(yt + u * d.stride) = f.step(hist, xu[u]);
+      for (int u = 0; u < U; ++u) g[u] = u < left ? __ldg(reinterpret_cast<const Raw*>(xt + u * xs)) : Vc::zero();
       xt += U * xs;
-      yt += U * d.stride;
-    }
-    if (left > 0) {
-      Raw xu[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) xu[u] = u < left ? __ldg(reinterpret_cast<const Raw*>(xt + u * xs)) : Vc::zero();
+    };
+    auto put = [&](const Raw* g, int n) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (u < left) *reinterpret_cast<Raw*>(yt + u * d.stride) = f.step(hist, xu[u]);
+        if (u < n) *reinterpret_cast<Raw*>(yt + u * d.stride) = f.step(hist, g[u]);
+      yt += U * d.stride;
+    };
+    fetch(xu[0]);
+    while (left > 0) {
+      int n = left;
+      left -= U;
+      fetch(xu[1]);
+      put(xu[0], n);
+      n = left;
+      left -= U;
+      fetch(xu[0]);
+      put(xu[1], n);
     }
   }
 }
 
 // One token of each row. A block takes a few rows and kThreadsIn vectors of channels (the
-// last row of blocks: their step sizes), so that the filter is loaded once for
+// last one of them: their step sizes), so that the filter is loaded once for
 // several rows. Into a decode layer (ring not null), v, k, Delta and a go to the record
 // that the row's next entry takes, (start + count) mod cap.
 template <typename IO, int W>
@@ -200,10 +210,11 @@ __global__ void __launch_bounds__(kThreadsIn) token_inputs_kernel(const __grid_c
   constexpr int R = 4;  // rows whose loads are in flight together
   pdl_enter();
   const Packed& pk = p.pk;
-  const bool steps = blockIdx.y == gridDim.y - 1;
-  const int c0 = ((int)blockIdx.y * kThreadsIn + (int)threadIdx.x) * V;
+  const int cols = p.col_blocks, col = blockIdx.x % cols;
+  const bool steps = col == cols - 1;
+  const int c0 = (col * kThreadsIn + (int)threadIdx.x) * V;
   const bool on = !steps && c0 < p.D;
-  const int r0 = (int)blockIdx.x * p.tile;
+  const int r0 = (int)(blockIdx.x / cols) * p.tile;
   const int r1 = r0 + p.tile < pk.n_seqs ? r0 + p.tile : pk.n_seqs;
   const int hp = p.H * p.P, gn = p.G * p.N;
   // what the vector belongs to: v of a head, k of a group or q; and its place in a ring record
@@ -315,7 +326,8 @@ cudaError_t launch_prompt_inputs(const InputsParams& in, int io, int num_sms, cu
   while (p.tile > 8 && (p.pk.tokens / p.tile * cb < 8 * num_sms || p.pk.tokens < (int64_t)p.tile * p.pk.n_seqs / 2))
     p.tile /= 2;
   const int64_t tiles = p.pk.tokens > 0 ? (p.pk.tokens + p.tile - 1) / p.tile : 1;
-  const dim3 grid((unsigned)tiles, cb + 1);
+  p.col_blocks = cb + 1;
+  const dim3 grid((unsigned)(tiles * p.col_blocks));
   return io == 1 ? prompt_io<__nv_bfloat16>(p, grid, s) : prompt_io<float>(p, grid, s);
 }
 
@@ -324,7 +336,8 @@ cudaError_t launch_token_inputs(const InputsParams& in, int io, int num_sms, cud
   const int cb = channel_blocks(p);
   p.tile = 4;  // rows of a block: the filter is loaded once for them
   while (p.tile > 1 && (int64_t)p.pk.n_seqs * cb < (int64_t)4 * num_sms * p.tile) p.tile /= 2;
-  const dim3 grid((unsigned)((p.pk.n_seqs + p.tile - 1) / p.tile), cb + 1);
+  p.col_blocks = cb + 1;
+  const dim3 grid((unsigned)((int64_t)(p.pk.n_seqs + p.tile - 1) / p.tile * p.col_blocks));
   return io == 1 ? token_io<__nv_bfloat16>(p, grid, s) : token_io<float>(p, grid, s);
 }
 

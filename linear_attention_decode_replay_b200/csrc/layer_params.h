@@ -23,6 +23,7 @@ struct InputsParams {
   Packed pk;  // token form: cu and resume are null, n_seqs rows of one token each
   int32_t H, G, P, N, D, width;
   int32_t tile;     // prompts: tokens of a block; token form: rows of a block
+  int32_t col_blocks;  // blocks of a tile: its channels', and one for the step sizes
   const void* x;    // [tokens] rows of D channels (v | k | q), ldx elements apart
   const void* raw;  // [tokens] rows of H raw step sizes, ldr elements apart
   int64_t ldx, ldr;
