@@ -107,7 +107,9 @@ int launch_scan(ScanParams& p, const replay_config& c, int64_t max_len, void* sc
   p.seg_tokens = sp.seg_tokens, p.max_segs = sp.max_segs;
   p.seg_state = static_cast<float*>(scratch);
   p.seg_decay = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + round256(segment_units(c, sp) * 64 * c.N * 4));
-  return launched(replay::launch_scan_tc(p, s));
+  int sms, rc;
+  if ((rc = sm_count(&sms))) return rc;
+  return launched(replay::launch_scan_tc(p, sms, s));
 }
 
 }  // namespace

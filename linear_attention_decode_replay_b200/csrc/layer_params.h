@@ -76,7 +76,7 @@ struct NormParams {
 cudaError_t launch_prompt_inputs(const InputsParams& p, int io, int num_sms, cudaStream_t s);
 cudaError_t launch_token_inputs(const InputsParams& p, int io, int num_sms, cudaStream_t s);
 cudaError_t launch_scan_serial(const ScanParams& p, int io, cudaStream_t s);
-cudaError_t launch_scan_tc(const ScanParams& p, cudaStream_t s);  // BF16, tokens > 0
+cudaError_t launch_scan_tc(const ScanParams& p, int num_sms, cudaStream_t s);  // BF16, tokens > 0
 // a decode layer's prefill: mask[b] = 1 where a sequence resumes row b; the read copy of
 // the served rows requantised from their checkpoints
 cudaError_t launch_resume_mask(const Packed& pk, uint8_t* mask, cudaStream_t s);

@@ -23,9 +23,9 @@ constexpr int kPT = 64;        // state rows of one block
 constexpr int kSplitSms = 148;  // the SMs that a split aims to fill
 constexpr int kTcThreads = 640;
 // Five warpgroups: 0 and 1 (rows of C, halves of the columns: P and the outputs), 2 (tokens:
-// decays and U), 3 (columns of the state), 4 (TMA and MMA). At 96 registers a thread at
+// decays and U), 3 (columns of the state), 4 (TMA, MMA and the plan). At 96 registers a thread at
 // launch, 2 and 4 give up what the state needs: (2 x 96 + 80 + 128 + 80) x 128 <= 5 x 96 x 128.
-constexpr int kWarpU = 8, kWarpS = 12, kWarpTma = 16, kWarpMmaQ = 17, kWarpMmaU = 18;
+constexpr int kWarpU = 8, kWarpS = 12, kWarpTma = 16, kWarpMmaQ = 17, kWarpMmaU = 18, kWarpPlan = 19;
 constexpr int kRegsLaunch = 96, kRegsTokens = 80, kRegsState = 128, kRegsCopy = 80;
 static_assert(2 * kRegsLaunch + kRegsTokens + kRegsState + kRegsCopy <= 5 * kRegsLaunch, "registers moved, not made");
 constexpr int kSlots = 3;  // chunks whose decays are held
@@ -34,16 +34,28 @@ struct alignas(64) ScanTcParams {
   CUtensorMap q, k, v;
   ScanParams s;
   int wide_y;  // rows of y start on 32-byte boundaries
+  int units;   // sequences (or segments) x heads x blocks of 64 rows; block b takes b, b + grid, ..
 };
 
 // Tensor memory columns. P lies over C: the two BF16 parts of 16 columns of P take the 16
 // columns that held C's.
 constexpr uint32_t kColC = 0, kColY1 = 128, kColY2 = 192, kColDS = 320;
 
+// A block's next unit: tokens [begin, begin + len) of one sequence, 64 state rows from p0 of
+// one head. len < 0: there is none.
+struct Unit {
+  int begin, len, h, g, p0, row, id;
+  int from, to;  // the state that it starts from and leaves: 0 zero / nowhere, 1 the caller's, 2 the segment's
+};
+constexpr int kSortSeqs = 64;  // up to as many sequences are taken longest first
+
 struct TcBars {
   uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t c_full, p_full, y_full, y_free, u_full, ds_full, ds_free, s_full, da_full[kSlots], drain[2];
+  uint64_t unit_full[2], unit_empty[2];
   uint32_t tmem, abort;
+  Unit unit[2];
+  int order[kSortSeqs];
 };
 // the decays of one chunk; "block" is 32 tokens
 struct alignas(16) Decays {
@@ -150,28 +162,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
     mbar_init(&bars->ds_full, 1), mbar_init(&bars->ds_free, 128);
     for (int i = 0; i < kSlots; ++i) mbar_init(&bars->da_full[i], 128);
     mbar_init(&bars->drain[0], 1), mbar_init(&bars->drain[1], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars->unit_full[i], 1), mbar_init(&bars->unit_empty[i], LOCAL ? 10 : 19);
     bars->abort = 0;
     fence_mbar_init();
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-
-  // the block's unit: sequence or segment of one, head, block of 64 state rows
-  const int ptiles = (p.P + kPT - 1) / kPT;
-  const int unit = blockIdx.x;
-  const int h = unit / ptiles % p.H, g = h / (p.H / p.G);
-  const int p0 = unit % ptiles * kPT;
-  int s = unit / (p.H * ptiles), seg = 0, segs = 1;
-  if (p.seg_tokens && !find_segment(p.pk, p.seg_tokens, s, s, seg, segs)) return;
-  if (LOCAL && seg == segs - 1) return;
-  int64_t begin, end;
-  if (!seq_bounds(p.pk, s, begin, end)) return;
-  if (segs > 1) {
-    begin += (int64_t)seg * p.seg_tokens;
-    if (seg < segs - 1) end = begin + p.seg_tokens;
-  }
-  const int row = seq_row(p.pk, s);
-  if (row < 0) return;
-  const int chunks = uniform((int)((end - begin + kChunk - 1) / kChunk));
 
   if (warp == kWarpTma) tmem_alloc(&bars->tmem, 512);
   tc_fence_before();
@@ -204,45 +199,117 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
     return __all_sync(0xffffffffu, wait2(bar0, phase0, bar1, phase1)) != 0;
   };
 
+  // the k-th unit (by a lane of its own, or a whole warp); its chunks, < 0 if there is none
+  auto take_unit = [&](Unit& u, int k) -> int {
+    if (!wait(&bars->unit_full[k & 1], k >> 1)) return -1;
+    u = bars->unit[k & 1];
+    mbar_arrive(&bars->unit_empty[k & 1]);
+    return u.len < 0 ? -1 : (u.len + kChunk - 1) / kChunk;
+  };
+  auto take_unit_warp = [&](Unit& u, int k) -> int {
+    if (!wait_warp(&bars->unit_full[k & 1], k >> 1)) return -1;
+    u = bars->unit[k & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->unit_empty[k & 1]);
+    return uniform(u.len < 0 ? -1 : (u.len + kChunk - 1) / kChunk);
+  };
+  // Every role walks the block's units and their chunks; n counts the chunks, over all units,
+  // and gives the phases of the barriers.
+
   if (warp >= kWarpTma) {
     regs_down<kRegsCopy>();
+    // ------------------------------------------------------------ plan
+    if (warp == kWarpPlan) {
+      const int ptiles = (p.P + kPT - 1) / kPT, heads = p.H * ptiles;
+      const bool sorted = !p.seg_tokens && p.pk.n_seqs <= kSortSeqs;
+      if (sorted) {
+        for (int s = lane; s < p.pk.n_seqs; s += 32) {
+          const int len = p.pk.cu[s + 1] - p.pk.cu[s];
+          int rank = 0;
+          for (int e = 0; e < p.pk.n_seqs; ++e) {
+            const int other = p.pk.cu[e + 1] - p.pk.cu[e];
+            rank += other > len || (other == len && e < s);
+          }
+          bars->order[rank] = s;
+        }
+        __syncwarp();
+      }
+      int k = 0;
+      bool more = true;
+#pragma unroll 1
+      for (int id = blockIdx.x; more; id += gridDim.x) {
+        Unit u;
+        u.len = -1;
+        more = id < tp.units;
+        if (more) {
+          int s = id / heads, seg = 0, segs = 1;
+          if (p.seg_tokens && !find_segment(p.pk, p.seg_tokens, s, s, seg, segs)) continue;
+          if (LOCAL && seg == segs - 1) continue;
+          if (sorted) s = bars->order[s];
+          int64_t begin, end;
+          if (!seq_bounds(p.pk, s, begin, end)) continue;
+          if (segs > 1) {
+            begin += (int64_t)seg * p.seg_tokens;
+            if (seg < segs - 1) end = begin + p.seg_tokens;
+          }
+          u.row = seq_row(p.pk, s);
+          if (u.row < 0) continue;
+          u.begin = (int)begin, u.len = (int)(end - begin);
+          u.h = id / ptiles % p.H, u.g = u.h / (p.H / p.G), u.p0 = id % ptiles * kPT;
+          u.id = id;
+          u.from = LOCAL ? 0 : segs > 1 ? 2 : p.pk.resume && p.pk.resume[s] ? 1 : 0;
+          u.to = LOCAL ? 2 : seg == segs - 1 ? 1 : 0;
+        }
+        if (k >= 2 && !wait_warp(&bars->unit_empty[k & 1], (k >> 1) - 1)) break;
+        if (lane == 0) {
+          bars->unit[k & 1] = u;
+          mbar_arrive(&bars->unit_full[k & 1]);
+        }
+        ++k;
+      }
+    }
     // ------------------------------------------------------------ TMA
     if (warp == kWarpTma && lane == 0) {
       // q of a chunk, then k and v of the next: the order in which their tiles fall free
-      int nq = 0, nk = 0, nv = 0;  // tiles issued
+      int n = 0, nq = 0;  // tiles of k and v, and of q, issued
+      Unit u;
+      int chunks = 0, c = 0, tq = -1, gq = 0;  // the chunk whose q is due: its first token and group
 #pragma unroll 1
-      for (int c = -1; c < chunks; ++c) {
-        const int t = (int)(begin + (int64_t)c * kChunk);
-        if (!LOCAL && c >= 0) {
-          if (c >= 1 && !wait(&bars->q_empty, c - 1)) break;
+      for (int k = 0; chunks >= 0;) {
+        while (chunks >= 0 && c >= chunks) chunks = take_unit(u, k++), c = 0;
+        const int t = u.begin + c * kChunk;
+        if (!LOCAL && tq >= 0) {
+          if (nq >= 1 && !wait(&bars->q_empty, nq - 1)) break;
           mbar_arrive_expect_tx(&bars->q_full, Lay::kQK);
 #pragma unroll 1
           for (int i = 0; i < NT / 64; ++i) {
-            tma_load3(smem + Lay::q + i * kTile, &tp.q, 64 * i, g, t, &bars->q_full);
+            tma_load3(smem + Lay::q + i * kTile, &tp.q, 64 * i, gq, tq, &bars->q_full);
             // q has one tile, so its next load starts late: from L2
-            if (c + 1 < chunks) tma_prefetch3(&tp.q, 64 * i, g, t + kChunk);
+            if (chunks >= 0) tma_prefetch3(&tp.q, 64 * i, u.g, t);
           }
           ++nq;
         }
-        const int n = c + 1, b = n & 1;
-        if (n < chunks) {
-          if (n >= 2 && !wait(&bars->k_empty[b], (n >> 1) - 1)) break;
-          mbar_arrive_expect_tx(&bars->k_full[b], Lay::kQK);
+        if (chunks < 0) break;
+        const int b = n & 1;
+        if (n >= 2 && !wait(&bars->k_empty[b], (n >> 1) - 1)) break;
+        mbar_arrive_expect_tx(&bars->k_full[b], Lay::kQK);
 #pragma unroll 1
-          for (int i = 0; i < NT / 64; ++i)
-            tma_load3(smem + Lay::k + b * Lay::kQK + i * kTile, &tp.k, 64 * i, g, t + kChunk, &bars->k_full[b]);
-          ++nk;
-          if (n >= 2 && !wait(&bars->v_empty[b], (n >> 1) - 1)) break;
-          mbar_arrive_expect_tx(&bars->v_full[b], kTile);
-          tma_load3(smem + Lay::v + b * kTile, &tp.v, p0, h, t + kChunk, &bars->v_full[b]);
-          ++nv;
+        for (int i = 0; i < NT / 64; ++i)
+          tma_load3(smem + Lay::k + b * Lay::kQK + i * kTile, &tp.k, 64 * i, u.g, t, &bars->k_full[b]);
+        if (n >= 2 && !wait(&bars->v_empty[b], (n >> 1) - 1)) {
+          mbar_wait_bounded(&bars->k_full[b], (n >> 1) & 1);
+          break;
         }
+        mbar_arrive_expect_tx(&bars->v_full[b], kTile);
+        tma_load3(smem + Lay::v + b * kTile, &tp.v, u.p0, u.h, t, &bars->v_full[b]);
+        ++n, ++c;
+        tq = t, gq = u.g;
       }
       if (*abort) {  // no copy may land after the block has gone
         if (nq) mbar_wait_bounded(&bars->q_full, (nq - 1) & 1);
         for (int b = 0; b < 2; ++b) {
-          if (nk > b) mbar_wait_bounded(&bars->k_full[b], ((nk - 1 - b) >> 1) & 1);
-          if (nv > b) mbar_wait_bounded(&bars->v_full[b], ((nv - 1 - b) >> 1) & 1);
+          if (n > b) mbar_wait_bounded(&bars->k_full[b], ((n - 1 - b) >> 1) & 1);
+          if (n > b) mbar_wait_bounded(&bars->v_full[b], ((n - 1 - b) >> 1) & 1);
         }
       }
     }
@@ -255,63 +322,75 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
     if (!LOCAL && warp == kWarpMmaQ) {
       const uint64_t dq = smem_desc(smem_u32(smem + Lay::q), 16);
       const uint64_t ds = smem_desc(smem_u32(smem + Lay::s), Lay::kSop);
+      Unit u;
+      int n = 0, chunks;
+      bool ok = true;
 #pragma unroll 1
-      for (int c = 0; c < chunks; ++c) {
-        const int b = c & 1;
-        const uint64_t dk = smem_desc(smem_u32(smem + Lay::k + b * Lay::kQK), 16);
-        // C = Q K^T, once Y1 is done with the last chunk's P in the same columns
-        if (!wait2_warp(&bars->q_full, c, &bars->k_full[b], c >> 1)) break;
-        if (c >= 1 && !wait_warp(&bars->y_full, c - 1)) break;
-        tc_fence_after();
-        if (elect_lane()) {
+      for (int k = 0; ok && (chunks = take_unit_warp(u, k)) >= 0; ++k) {
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c, ++n) {
+          const int b = n & 1;
+          const uint64_t dk = smem_desc(smem_u32(smem + Lay::k + b * Lay::kQK), 16);
+          // C = Q K^T, once Y1 is done with the last chunk's P in the same columns
+          if (!(ok = wait2_warp(&bars->q_full, n, &bars->k_full[b], n >> 1))) break;
+          if (n >= 1 && !(ok = wait_warp(&bars->y_full, n - 1))) break;
+          tc_fence_after();
+          if (elect_lane()) {
 #pragma unroll 2
-          for (int i = 0; i < NT / 16; ++i) {
-            const int at = (i / 4 * kTile + i % 4 * 32) >> 4;
-            mma_ss(tmem + kColC, dq + at, dk + at, kC, i > 0);
+            for (int i = 0; i < NT / 16; ++i) {
+              const int at = (i / 4 * kTile + i % 4 * 32) >> 4;
+              mma_ss(tmem + kColC, dq + at, dk + at, kC, i > 0);
+            }
+            mma_commit(&bars->c_full);
           }
-          mma_commit(&bars->c_full);
-        }
-        // Y2 = Q S^T, the state's two parts side by side, once the last chunk's outputs have been read
-        if (!wait_warp(&bars->s_full, c) || (c >= 1 && !wait_warp(&bars->y_free, c - 1))) break;
-        tc_fence_after();
-        if (elect_lane()) {
+          // Y2 = Q S^T, the state's two parts side by side, once the last chunk's outputs have been read
+          if (!(ok = wait_warp(&bars->s_full, n) && (n == 0 || wait_warp(&bars->y_free, n - 1)))) break;
+          tc_fence_after();
+          if (elect_lane()) {
 #pragma unroll 2
-          for (int i = 0; i < NT / 16; ++i)
-            mma_ss(tmem + kColY2, dq + ((i / 4 * kTile + i % 4 * 32) >> 4), ds + i * 128, kY2, i > 0);
-          mma_commit(&bars->q_empty);
-          mma_commit(&bars->k_empty[b]);
+            for (int i = 0; i < NT / 16; ++i)
+              mma_ss(tmem + kColY2, dq + ((i / 4 * kTile + i % 4 * 32) >> 4), ds + i * 128, kY2, i > 0);
+            mma_commit(&bars->q_empty);
+            mma_commit(&bars->k_empty[b]);
+          }
         }
       }
     } else if (warp == kWarpMmaU) {
       const uint64_t du = smem_desc(smem_u32(smem + Lay::u), kTile);
+      Unit u;
+      int n = 0, chunks;
+      bool ok = true;
 #pragma unroll 1
-      for (int c = 0; c < chunks; ++c) {
-        const int b = c & 1;
-        const uint64_t dk = smem_desc(smem_u32(smem + Lay::k + b * Lay::kQK), kTile);
-        const uint64_t dv = smem_desc(smem_u32(smem + Lay::v + b * kTile), 16);
-        // dS = K^T U, the three parts side by side
-        if (!wait2_warp(&bars->u_full, c, &bars->k_full[b], c >> 1)) break;
-        if (c >= 1 && !wait_warp(&bars->ds_free, c - 1)) break;
-        tc_fence_after();
-        if (elect_lane()) {
+      for (int k = 0; ok && (chunks = take_unit_warp(u, k)) >= 0; ++k) {
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c, ++n) {
+          const int b = n & 1;
+          const uint64_t dk = smem_desc(smem_u32(smem + Lay::k + b * Lay::kQK), kTile);
+          const uint64_t dv = smem_desc(smem_u32(smem + Lay::v + b * kTile), 16);
+          // dS = K^T U, the three parts side by side
+          if (!(ok = wait2_warp(&bars->u_full, n, &bars->k_full[b], n >> 1))) break;
+          if (n >= 1 && !(ok = wait_warp(&bars->ds_free, n - 1))) break;
+          tc_fence_after();
+          if (elect_lane()) {
 #pragma unroll 2
-          for (int i = 0; i < kChunk / 16; ++i) mma_ss(tmem + kColDS, dk + i * 128, du + i * 128, kDS, i > 0);
-          mma_commit(&bars->ds_full);
-          mma_commit(&bars->k_empty[b]);
-        }
-        if (LOCAL) continue;
-        // Y1 = P V
-        if (!wait2_warp(&bars->p_full, c, &bars->v_full[b], c >> 1)) break;
-        tc_fence_after();
-        if (elect_lane()) {
-#pragma unroll 2
-          for (int i = 0; i < kChunk / 16; ++i) {
-            const uint32_t pa = tmem + kColC + i * 16;
-            mma_ts(tmem + kColY1, pa, dv + i * 128, kY1, i > 0);
-            mma_ts(tmem + kColY1, pa + 8, dv + i * 128, kY1, true);
+            for (int i = 0; i < kChunk / 16; ++i) mma_ss(tmem + kColDS, dk + i * 128, du + i * 128, kDS, i > 0);
+            mma_commit(&bars->ds_full);
+            mma_commit(&bars->k_empty[b]);
           }
-          mma_commit(&bars->y_full);
-          mma_commit(&bars->v_empty[b]);
+          if (LOCAL) continue;
+          // Y1 = P V
+          if (!(ok = wait2_warp(&bars->p_full, n, &bars->v_full[b], n >> 1))) break;
+          tc_fence_after();
+          if (elect_lane()) {
+#pragma unroll 2
+            for (int i = 0; i < kChunk / 16; ++i) {
+              const uint32_t pa = tmem + kColC + i * 16;
+              mma_ts(tmem + kColY1, pa, dv + i * 128, kY1, i > 0);
+              mma_ts(tmem + kColY1, pa + 8, dv + i * 128, kY1, true);
+            }
+            mma_commit(&bars->y_full);
+            mma_commit(&bars->v_empty[b]);
+          }
         }
       }
     }
@@ -324,114 +403,121 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
     const int w4 = warp & 3, half = warp >> 2;
     const int i = w4 * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(w4 * 32) << 16);
+    Unit u;
+    int n = 0, chunks;
+    bool ok = !LOCAL;
 #pragma unroll 1
-    for (int c = 0; c < (LOCAL ? 0 : chunks); ++c) {
-      const Decays& d = dec[c % kSlots];
-      if (!wait2_warp(&bars->da_full[c % kSlots], c / kSlots, &bars->c_full, c)) break;
-      tc_fence_after();
-      const float pre = d.pre[i];
-      // Half 0 takes the diagonal block of 32 columns, half 1 those before it. The loops stay small: four warps with code of their own
-      // share an instruction cache, and unrolled they waited for instructions.
-      if (half == 0) {
-        const float4* da = reinterpret_cast<const float4*>(d.da + 32 * w4);
-        float rd = 0.f;
+    for (int k = 0; ok && (chunks = take_unit_warp(u, k)) >= 0; ++k) {
+      const int64_t end = (int64_t)u.begin + u.len;
 #pragma unroll 1
-        for (int j0 = 16; j0 >= 0; j0 -= 16) {  // products from j = i down
-          uint32_t x[16], hi[8], lo[8];
-          tmem_ld16(tl + kColC + 32 * w4 + j0, x);
-          tmem_wait_ld16(x);
+      for (int c = 0; c < chunks; ++c, ++n) {
+        const Decays& d = dec[n % kSlots];
+        if (!(ok = wait2_warp(&bars->da_full[n % kSlots], n / kSlots, &bars->c_full, n))) break;
+        tc_fence_after();
+        const float pre = d.pre[i];
+        // Half 0 takes the diagonal block of 32 columns, half 1 those before it. The loops stay small: four warps with code of their own
+        // share an instruction cache, and unrolled they waited for instructions.
+        if (half == 0) {
+          const float4* da = reinterpret_cast<const float4*>(d.da + 32 * w4);
+          float rd = 0.f;
+#pragma unroll 1
+          for (int j0 = 16; j0 >= 0; j0 -= 16) {  // products from j = i down
+            uint32_t x[16], hi[8], lo[8];
+            tmem_ld16(tl + kColC + 32 * w4 + j0, x);
+            tmem_wait_ld16(x);
 #pragma unroll
-          for (int j = 14; j >= 0; j -= 2) {
-            const float4 u = da[(j0 + j) / 2];  // a_{j+1}, Delta_j, a_{j+2}, Delta_{j+1}
-            rd = j + 1 == lane - j0 ? 1.f : rd * u.z;
-            const float f1 = j + 1 <= lane - j0 ? __uint_as_float(x[j + 1]) * (rd * u.w) : 0.f;
-            rd = j == lane - j0 ? 1.f : rd * u.x;
-            const float f0 = j <= lane - j0 ? __uint_as_float(x[j]) * (rd * u.y) : 0.f;
-            f32x2 f = pair(f0, f1);
-            hi[j / 2] = take_part(f);
-            lo[j / 2] = last_part(f);
+            for (int j = 14; j >= 0; j -= 2) {
+              const float4 w = da[(j0 + j) / 2];  // a_{j+1}, Delta_j, a_{j+2}, Delta_{j+1}
+              rd = j + 1 == lane - j0 ? 1.f : rd * w.z;
+              const float f1 = j + 1 <= lane - j0 ? __uint_as_float(x[j + 1]) * (rd * w.w) : 0.f;
+              rd = j == lane - j0 ? 1.f : rd * w.x;
+              const float f0 = j <= lane - j0 ? __uint_as_float(x[j]) * (rd * w.y) : 0.f;
+              f32x2 f = pair(f0, f1);
+              hi[j / 2] = take_part(f);
+              lo[j / 2] = last_part(f);
+            }
+            tmem_st8(tl + kColC + 32 * w4 + j0, hi);
+            tmem_st8(tl + kColC + 32 * w4 + j0 + 8, lo);
           }
-          tmem_st8(tl + kColC + 32 * w4 + j0, hi);
-          tmem_st8(tl + kColC + 32 * w4 + j0 + 8, lo);
-        }
-      } else {
-        const uint32_t zero[8] = {0};
-#pragma unroll 1
-        for (int x = 32 * (w4 + 1); x < kChunk; x += 8) tmem_st8(tl + kColC + x, zero);  // later tokens
-      }
-      float r = pre;  // from the block's end up to i
-#pragma unroll 1
-      for (int cb = half == 0 ? -1 : w4 - 1; cb >= 0; --cb) {
-        uint32_t x[32];
-        tmem_ld32(tl + kColC + 32 * cb, x);
-        const ulonglong2* gv = reinterpret_cast<const ulonglong2*>(d.g + 32 * cb);
-        const f32x2 rr = pair(r, r);
-        r *= d.total[cb];
-        tmem_wait_ld32(x);
-#pragma unroll
-        for (int j0 = 0; j0 < 32; j0 += 16) {
-          uint32_t hi[8], lo[8];
-#pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const ulonglong2 e = gv[(j0 + j) / 4];
-            f32x2 f = mul2(pair(__uint_as_float(x[j0 + j]), __uint_as_float(x[j0 + j + 1])), mul2(rr, e.x));
-            hi[j / 2] = take_part(f);
-            lo[j / 2] = last_part(f);
-            f = mul2(pair(__uint_as_float(x[j0 + j + 2]), __uint_as_float(x[j0 + j + 3])), mul2(rr, e.y));
-            hi[j / 2 + 1] = take_part(f);
-            lo[j / 2 + 1] = last_part(f);
-          }
-          tmem_st8(tl + kColC + 32 * cb + j0, hi);
-          tmem_st8(tl + kColC + 32 * cb + j0 + 8, lo);
-        }
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&bars->p_full);
-
-      float abar = pre;
-#pragma unroll
-      for (int x = 0; x < 3; ++x)
-        if (x < w4) abar *= d.total[x];
-      if (!wait2_warp(&bars->y_full, c, &bars->q_empty, c)) break;
-      tc_fence_after();
-      const bool bad = d.bad != 0;
-      const int64_t t = begin + (int64_t)c * kChunk + i;
-      __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + ((size_t)t * p.H + h) * p.P + p0 + 32 * half;
-      const f32x2 ab = pair(abar, abar);
-#pragma unroll 1
-      for (int part = 0; part < 2; ++part) {
-        uint32_t y1[16], y2[16], y3[16], o[8];
-        tmem_ld16(tl + kColY1 + 32 * half + 16 * part, y1);
-        tmem_ld16(tl + kColY2 + 32 * half + 16 * part, y2);
-        tmem_ld16(tl + kColY2 + kPT + 32 * half + 16 * part, y3);
-        tmem_wait_ld16(y1);
-        tmem_wait_ld16(y2);
-        tmem_wait_ld16(y3);
-        if (part == 1) {
-          tc_fence_before();
-          mbar_arrive(&bars->y_free);
-        }
-#pragma unroll
-        for (int j = 0; j < 16; j += 2)
-          o[j / 2] = last_part(fma2(ab, add2(reg_pair(y2 + j), reg_pair(y3 + j)), reg_pair(y1 + j)));
-        const int left = t < end ? p.P - (p0 + 32 * half + 16 * part) : 0;  // of the head's rows p
-        if (left >= 16 && tp.wide_y) {
-          store_sector(y + 16 * part, o);
         } else {
-          if (left > 0) *reinterpret_cast<uint4*>(y + 16 * part) = make_uint4(o[0], o[1], o[2], o[3]);
-          if (left > 8) *reinterpret_cast<uint4*>(y + 16 * part + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+          const uint32_t zero[8] = {0};
+#pragma unroll 1
+          for (int x = 32 * (w4 + 1); x < kChunk; x += 8) tmem_st8(tl + kColC + x, zero);  // later tokens
         }
-      }
-      if (bad && t < end) {
-        // the products saw zeros in place of what is not finite in v: it reaches every later row
-        const uint16_t* v = static_cast<const uint16_t*>(p.v) + p0 + 32 * half;
+        float r = pre;  // from the block's end up to i
 #pragma unroll 1
-        for (int j = 0; j <= i; ++j) {
-          const uint16_t* vj = v + ((size_t)(t - i + j) * p.H + h) * p.P;
+        for (int cb = half == 0 ? -1 : w4 - 1; cb >= 0; --cb) {
+          uint32_t x[32];
+          tmem_ld32(tl + kColC + 32 * cb, x);
+          const ulonglong2* gv = reinterpret_cast<const ulonglong2*>(d.g + 32 * cb);
+          const f32x2 rr = pair(r, r);
+          r *= d.total[cb];
+          tmem_wait_ld32(x);
+#pragma unroll
+          for (int j0 = 0; j0 < 32; j0 += 16) {
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+              const ulonglong2 e = gv[(j0 + j) / 4];
+              f32x2 f = mul2(pair(__uint_as_float(x[j0 + j]), __uint_as_float(x[j0 + j + 1])), mul2(rr, e.x));
+              hi[j / 2] = take_part(f);
+              lo[j / 2] = last_part(f);
+              f = mul2(pair(__uint_as_float(x[j0 + j + 2]), __uint_as_float(x[j0 + j + 3])), mul2(rr, e.y));
+              hi[j / 2 + 1] = take_part(f);
+              lo[j / 2 + 1] = last_part(f);
+            }
+            tmem_st8(tl + kColC + 32 * cb + j0, hi);
+            tmem_st8(tl + kColC + 32 * cb + j0 + 8, lo);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars->p_full);
+
+        float abar = pre;
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+          if (x < w4) abar *= d.total[x];
+        if (!(ok = wait2_warp(&bars->y_full, n, &bars->q_empty, n))) break;
+        tc_fence_after();
+        const bool bad = d.bad != 0;
+        const int64_t t = u.begin + (int64_t)c * kChunk + i;
+        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + ((size_t)t * p.H + u.h) * p.P + u.p0 + 32 * half;
+        const f32x2 ab = pair(abar, abar);
 #pragma unroll 1
-          for (int e = 0; e < 32 && p0 + 32 * half + e < p.P; ++e)
-            if ((vj[e] & 0x7F80) == 0x7F80) reinterpret_cast<uint16_t*>(y)[e] = 0x7FC0;
+        for (int part = 0; part < 2; ++part) {
+          uint32_t y1[16], y2[16], y3[16], o[8];
+          tmem_ld16(tl + kColY1 + 32 * half + 16 * part, y1);
+          tmem_ld16(tl + kColY2 + 32 * half + 16 * part, y2);
+          tmem_ld16(tl + kColY2 + kPT + 32 * half + 16 * part, y3);
+          tmem_wait_ld16(y1);
+          tmem_wait_ld16(y2);
+          tmem_wait_ld16(y3);
+          if (part == 1) {
+            tc_fence_before();
+            mbar_arrive(&bars->y_free);
+          }
+#pragma unroll
+          for (int j = 0; j < 16; j += 2)
+            o[j / 2] = last_part(fma2(ab, add2(reg_pair(y2 + j), reg_pair(y3 + j)), reg_pair(y1 + j)));
+          const int left = t < end ? p.P - (u.p0 + 32 * half + 16 * part) : 0;  // of the head's rows p
+          if (left >= 16 && tp.wide_y) {
+            store_sector(y + 16 * part, o);
+          } else {
+            if (left > 0) *reinterpret_cast<uint4*>(y + 16 * part) = make_uint4(o[0], o[1], o[2], o[3]);
+            if (left > 8) *reinterpret_cast<uint4*>(y + 16 * part + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+        }
+        if (bad && t < end) {
+          // the products saw zeros in place of what is not finite in v: it reaches every later row
+          const uint16_t* v = static_cast<const uint16_t*>(p.v) + u.p0 + 32 * half;
+#pragma unroll 1
+          for (int j = 0; j <= i; ++j) {
+            const uint16_t* vj = v + ((size_t)(t - i + j) * p.H + u.h) * p.P;
+#pragma unroll 1
+            for (int e = 0; e < 32 && u.p0 + 32 * half + e < p.P; ++e)
+              if ((vj[e] & 0x7F80) == 0x7F80) reinterpret_cast<uint16_t*>(y)[e] = 0x7FC0;
+          }
         }
       }
     }
@@ -440,110 +526,108 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
     regs_down<kRegsTokens>();
     const int j = threadIdx.x - 32 * kWarpU, w4 = warp - kWarpU;
     float a = 1.f, dt = 0.f;
-    auto load_da = [&](int c) {  // this thread's token of chunk c; past the sequence: no decay, no step
-      const int64_t t = begin + (int64_t)c * kChunk + j;
-      const bool in = c < chunks && t < end;
-      a = in ? p.a[(size_t)t * p.H + h] : 1.f;
-      dt = in ? p.dt[(size_t)t * p.H + h] : 0.f;
-    };
-    load_da(0);
+    Unit u;
+    int n = 0, chunks;
+    bool ok = true;
 #pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
-      const int b = c & 1;
-      Decays& d = dec[c % kSlots];
-      const int len = (int)(end - begin - (int64_t)c * kChunk < kChunk ? end - begin - (int64_t)c * kChunk : kChunk);
-      // products of the decays up to and after this token, in its block and then over the chunk
-      float pre = a, suf = a;
+    for (int k = 0; ok && (chunks = take_unit_warp(u, k)) >= 0; ++k) {
+      const int64_t end = (int64_t)u.begin + u.len;
+      auto load_da = [&](int c) {  // this thread's token of chunk c; past the sequence: no decay, no step
+        const int64_t t = u.begin + (int64_t)c * kChunk + j;
+        const bool in = c < chunks && t < end;
+        a = in ? p.a[(size_t)t * p.H + u.h] : 1.f;
+        dt = in ? p.dt[(size_t)t * p.H + u.h] : 0.f;
+      };
+      load_da(0);
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c, ++n) {
+        const int b = n & 1;
+        Decays& d = dec[n % kSlots];
+        const int len = u.len - c * kChunk < kChunk ? u.len - c * kChunk : kChunk;
+        // products of the decays up to and after this token, in its block and then over the chunk
+        float pre = a, suf = a;
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const float u = __shfl_up_sync(0xffffffffu, pre, off), f = __shfl_down_sync(0xffffffffu, suf, off);
-        if (lane >= off) pre *= u;
-        if (lane + off < 32) suf *= f;
-      }
-      suf = __shfl_down_sync(0xffffffffu, suf, 1);
-      if (lane == 31) suf = 1.f;
-      if (lane == 31) d.total[w4] = pre;
-      if (j == 0) d.bad = 0;
-      d.pre[j] = pre;
-      d.g[j] = dt * suf;
-      d.da[j].y = dt;
-      if (j > 0) d.da[j - 1].x = a;
-      if (j == kChunk - 1) d.da[j].x = 1.f;
-      mbar_arrive(&bars->da_full[c % kSlots]);
-      if (!wait_warp(&bars->da_full[c % kSlots], c / kSlots)) break;
-      float wj = dt * suf;
+        for (int off = 1; off < 32; off <<= 1) {
+          const float e = __shfl_up_sync(0xffffffffu, pre, off), f = __shfl_down_sync(0xffffffffu, suf, off);
+          if (lane >= off) pre *= e;
+          if (lane + off < 32) suf *= f;
+        }
+        suf = __shfl_down_sync(0xffffffffu, suf, 1);
+        if (lane == 31) suf = 1.f;
+        if (lane == 31) d.total[w4] = pre;
+        if (j == 0) d.bad = 0;
+        d.pre[j] = pre;
+        d.g[j] = dt * suf;
+        d.da[j].y = dt;
+        if (j > 0) d.da[j - 1].x = a;
+        if (j == kChunk - 1) d.da[j].x = 1.f;
+        mbar_arrive(&bars->da_full[n % kSlots]);
+        if (!(ok = wait_warp(&bars->da_full[n % kSlots], n / kSlots))) break;
+        float wj = dt * suf;
 #pragma unroll
-      for (int x = 1; x < 4; ++x)
-        if (x > w4) wj *= d.total[x];
-      load_da(c + 1);
+        for (int x = 1; x < 4; ++x)
+          if (x > w4) wj *= d.total[x];
+        load_da(c + 1);
 
-      if (!wait_warp(&bars->v_full[b], c >> 1)) break;
-      if (c >= 1 && !wait_warp(&bars->ds_full, c - 1)) break;  // U's last values have been read
-      uint8_t* vrow = smem + Lay::v + b * kTile + j * 128;
-      uint8_t* urow = smem + Lay::u + j * 128;
-      if (len < kChunk && !wait_warp(&bars->k_full[b], c >> 1)) break;
-      if (j >= len) {
-        // another sequence's tokens: zeros in v and k (0 times its NaN would be NaN)
-        for (int x = 0; x < 8; ++x) *reinterpret_cast<uint4*>(vrow + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
-        for (int i = 0; i < NT / 64; ++i)
-          for (int x = 0; x < 8; ++x)
-            *reinterpret_cast<uint4*>(smem + Lay::k + b * Lay::kQK + i * kTile + j * 128 + 16 * x) =
-                make_uint4(0u, 0u, 0u, 0u);
-      }
-      const f32x2 ww = pair(wj, wj);
-      f32x2 check[2] = {0, 0};  // 0 times what is not finite is NaN
+        if (!(ok = wait_warp(&bars->v_full[b], n >> 1))) break;
+        if (n >= 1 && !(ok = wait_warp(&bars->ds_full, n - 1))) break;  // U's last values have been read
+        uint8_t* vrow = smem + Lay::v + b * kTile + j * 128;
+        uint8_t* urow = smem + Lay::u + j * 128;
+        if (len < kChunk && !(ok = wait_warp(&bars->k_full[b], n >> 1))) break;
+        if (j >= len) {
+          // another sequence's tokens: zeros in v and k (0 times its NaN would be NaN)
+          for (int x = 0; x < 8; ++x) *reinterpret_cast<uint4*>(vrow + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
+          for (int i = 0; i < NT / 64; ++i)
+            for (int x = 0; x < 8; ++x)
+              *reinterpret_cast<uint4*>(smem + Lay::k + b * Lay::kQK + i * kTile + j * 128 + 16 * x) =
+                  make_uint4(0u, 0u, 0u, 0u);
+        }
+        const f32x2 ww = pair(wj, wj);
+        f32x2 check[2] = {0, 0};  // 0 times what is not finite is NaN
 #pragma unroll 2
-      for (int x = 0; x < 8; ++x) {
-        const int at = (x ^ (j & 7)) << 4;
-        const uint4 vu = *reinterpret_cast<const uint4*>(vrow + at);
-        float f[8];
-        Vec<__nv_bfloat16>::unpack(vu, f);
-        uint32_t u1[4], u2[4], u3[4];
+        for (int x = 0; x < 8; ++x) {
+          const int at = (x ^ (j & 7)) << 4;
+          const uint4 vu = *reinterpret_cast<const uint4*>(vrow + at);
+          float f[8];
+          Vec<__nv_bfloat16>::unpack(vu, f);
+          uint32_t u1[4], u2[4], u3[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const f32x2 v2 = pair(f[2 * e], f[2 * e + 1]);
-          check[e & 1] = fma2(v2, 0, check[e & 1]);
-          f32x2 u = mul2(v2, ww);
-          u1[e] = take_part(u);
-          u2[e] = take_part(u);
-          u3[e] = last_part(u);
+          for (int e = 0; e < 4; ++e) {
+            const f32x2 v2 = pair(f[2 * e], f[2 * e + 1]);
+            check[e & 1] = fma2(v2, 0, check[e & 1]);
+            f32x2 part = mul2(v2, ww);
+            u1[e] = take_part(part);
+            u2[e] = take_part(part);
+            u3[e] = last_part(part);
+          }
+          *reinterpret_cast<uint4*>(urow + at) = make_uint4(u1[0], u1[1], u1[2], u1[3]);
+          *reinterpret_cast<uint4*>(urow + kTile + at) = make_uint4(u2[0], u2[1], u2[2], u2[3]);
+          *reinterpret_cast<uint4*>(urow + 2 * kTile + at) = make_uint4(u3[0], u3[1], u3[2], u3[3]);
         }
-        *reinterpret_cast<uint4*>(urow + at) = make_uint4(u1[0], u1[1], u1[2], u1[3]);
-        *reinterpret_cast<uint4*>(urow + kTile + at) = make_uint4(u2[0], u2[1], u2[2], u2[3]);
-        *reinterpret_cast<uint4*>(urow + 2 * kTile + at) = make_uint4(u3[0], u3[1], u3[2], u3[3]);
-      }
-      float c0, c1;
-      unpair(add2(check[0], check[1]), c0, c1);
-      if (!LOCAL && c0 + c1 != 0.f) {
-        // what is not finite must not meet the zeros of the earlier tokens' rows of P
+        float c0, c1;
+        unpair(add2(check[0], check[1]), c0, c1);
+        if (!LOCAL && c0 + c1 != 0.f) {
+          // what is not finite must not meet the zeros of the earlier tokens' rows of P
 #pragma unroll 1
-        for (int x = 0; x < 64; ++x) {
-          uint16_t* e = reinterpret_cast<uint16_t*>(vrow) + x;
-          if ((*e & 0x7F80) == 0x7F80) *e = 0;
+          for (int x = 0; x < 64; ++x) {
+            uint16_t* e = reinterpret_cast<uint16_t*>(vrow) + x;
+            if ((*e & 0x7F80) == 0x7F80) *e = 0;
+          }
+          d.bad = 1;
         }
-        d.bad = 1;
+        fence_async_smem();
+        mbar_arrive(&bars->u_full);
+        if (LOCAL) mbar_arrive(&bars->v_empty[b]);
       }
-      fence_async_smem();
-      mbar_arrive(&bars->u_full);
-      if (LOCAL) mbar_arrive(&bars->v_empty[b]);
     }
   } else if (warp < kWarpTma) {
     // ------------------------------------------------------------ the state: column n
     regs_up<kRegsState>();
-    const int n = threadIdx.x - 32 * kWarpS, w4 = warp - kWarpS;
+    const int sn = threadIdx.x - 32 * kWarpS, w4 = warp - kWarpS;  // column n
     const uint32_t tl = tmem + ((uint32_t)(w4 * 32) << 16);
     f32x2 S[kPT / 2];
-    // rows p of the state that it starts from: the caller's, a segment's, or zero
-    float* Sg = p.S + (((size_t)row * p.H + h) * p.P + p0) * p.N + n;
-    float* Eg = p.seg_state + (size_t)unit * kPT * p.N + n;
-    const float* from = segs > 1 ? Eg : Sg;
-    const bool res = !LOCAL && n < p.N && (segs > 1 || (p.pk.resume && p.pk.resume[s]));
-#pragma unroll
-    for (int e = 0; e < kPT; e += 2)  // P is a multiple of 8
-      S[e / 2] = res && p0 + e < p.P ? pair(from[(size_t)e * p.N], from[(size_t)(e + 1) * p.N]) : 0;
-    float decay = 1.f;
     // 16 rows p of the state's two BF16 parts as an operand: row n, chunk x at x ^ (n % 8)
-    uint8_t* dst = smem + Lay::s + n * 128;
+    uint8_t* dst = smem + Lay::s + sn * 128;
     auto put_state = [&](int part) {
 #pragma unroll
       for (int x = 2 * part; x < 2 * part + 2; ++x) {
@@ -554,60 +638,79 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
           hi[e] = take_part(f);
           lo[e] = last_part(f);
         }
-        uint8_t* at = dst + ((x ^ (n & 7)) << 4);
+        uint8_t* at = dst + ((x ^ (sn & 7)) << 4);
         *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(at + Lay::kSop) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
     };
-    if (!LOCAL && n < NT) {
-#pragma unroll
-      for (int part = 0; part < 4; ++part) put_state(part);
-    }
-    fence_async_smem();
-    mbar_arrive(&bars->s_full);
+    Unit u;
+    int n = 0, chunks;
+    bool ok = true;
 #pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
-      // dS is there, and Y2 has read the state's operand
-      if (LOCAL ? !wait_warp(&bars->ds_full, c) : !wait2_warp(&bars->ds_full, c, &bars->q_empty, c)) break;
-      tc_fence_after();
-      const float* tot = dec[c % kSlots].total;
-      const float all = (tot[0] * tot[1]) * (tot[2] * tot[3]);
-      const f32x2 all2 = pair(all, all);
-      if (LOCAL) decay *= all;
+    for (int k = 0; ok && (chunks = take_unit_warp(u, k)) >= 0; ++k) {
+      // rows p of the state that it starts from: the caller's, a segment's, or zero
+      float* Sg = p.S + (((size_t)u.row * p.H + u.h) * p.P + u.p0) * p.N + sn;
+      float* Eg = p.seg_state + (size_t)u.id * kPT * p.N + sn;
+      const int rows = sn < p.N ? p.P - u.p0 : 0;  // P is a multiple of 8
+      const float* from = u.from == 2 ? Eg : Sg;
 #pragma unroll
-      for (int part = 0; part < 4; ++part) {
-        uint32_t d1[16], d2[16], d3[16];
-        tmem_ld16(tl + kColDS + 16 * part, d1);
-        tmem_ld16(tl + kColDS + kPT + 16 * part, d2);
-        tmem_ld16(tl + kColDS + 2 * kPT + 16 * part, d3);
-        tmem_wait_ld16(d1);
-        tmem_wait_ld16(d2);
-        tmem_wait_ld16(d3);
+      for (int e = 0; e < kPT; e += 2)
+        S[e / 2] = u.from && e < rows ? pair(from[(size_t)e * p.N], from[(size_t)(e + 1) * p.N]) : 0;
+      float decay = 1.f;
+      if (!LOCAL && chunks > 0) {  // the last chunk's Y2 has read the operand
+        if (sn < NT) {
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          f32x2& x = S[8 * part + e / 2];
-          x = fma2(all2, x, add2(reg_pair(d1 + e), add2(reg_pair(d2 + e), reg_pair(d3 + e))));
+          for (int part = 0; part < 4; ++part) put_state(part);
         }
-        if (!LOCAL && n < NT) put_state(part);
+        fence_async_smem();
+        mbar_arrive(&bars->s_full);
       }
-      tc_fence_before();
-      mbar_arrive(&bars->ds_free);
-      fence_async_smem();
-      mbar_arrive(&bars->s_full);
-    }
-    if (!*abort && (LOCAL || seg == segs - 1)) {
-      float* to = LOCAL ? Eg : Sg;
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c, ++n) {
+        // dS is there, and Y2 has read the state's operand
+        if (!(ok = LOCAL ? wait_warp(&bars->ds_full, n) : wait2_warp(&bars->ds_full, n, &bars->q_empty, n))) break;
+        tc_fence_after();
+        const float* tot = dec[n % kSlots].total;
+        const float all = (tot[0] * tot[1]) * (tot[2] * tot[3]);
+        const f32x2 all2 = pair(all, all);
+        if (LOCAL) decay *= all;
+        const bool put = !LOCAL && c + 1 < chunks;
+#pragma unroll
+        for (int part = 0; part < 4; ++part) {
+          uint32_t d1[16], d2[16], d3[16];
+          tmem_ld16(tl + kColDS + 16 * part, d1);
+          tmem_ld16(tl + kColDS + kPT + 16 * part, d2);
+          tmem_ld16(tl + kColDS + 2 * kPT + 16 * part, d3);
+          tmem_wait_ld16(d1);
+          tmem_wait_ld16(d2);
+          tmem_wait_ld16(d3);
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            f32x2& x = S[8 * part + e / 2];
+            x = fma2(all2, x, add2(reg_pair(d1 + e), add2(reg_pair(d2 + e), reg_pair(d3 + e))));
+          }
+          if (put && sn < NT) put_state(part);
+        }
+        tc_fence_before();
+        mbar_arrive(&bars->ds_free);
+        if (put) {
+          fence_async_smem();
+          mbar_arrive(&bars->s_full);
+        }
+      }
+      if (!ok || !u.to) continue;
+      float* to = u.to == 2 ? Eg : Sg;
 #pragma unroll
       for (int e = 0; e < kPT; e += 2) {
         float s0, s1;
         unpair(S[e / 2], s0, s1);
-        if (n < p.N && p0 + e < p.P) {
+        if (e < rows) {
           to[(size_t)e * p.N] = s0;
           to[(size_t)(e + 1) * p.N] = s1;
         }
       }
-      if (LOCAL && n == 0) p.seg_decay[unit] = decay;
-      if (!LOCAL && p.counts && h == 0 && p0 == 0 && n == 0) p.counts[row] = 0;
+      if (LOCAL && sn == 0) p.seg_decay[u.id] = decay;
+      if (!LOCAL && p.counts && u.h == 0 && u.p0 == 0 && sn == 0) p.counts[u.row] = 0;
     }
   }
   __syncwarp();
@@ -704,7 +807,7 @@ bool tile_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int w
 }
 
 template <int NT, bool LOCAL>
-cudaError_t launch_tc(const ScanTcParams& tp, int64_t units, cudaStream_t s) {
+cudaError_t launch_tc(ScanTcParams& tp, int64_t units, int num_sms, cudaStream_t s) {
   constexpr int smem = TcLayout<NT>::bytes;
   static bool configured[64] = {false};  // per device; setting it twice does no harm
   int dev = 0;
@@ -715,19 +818,20 @@ cudaError_t launch_tc(const ScanTcParams& tp, int64_t units, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) configured[dev] = true;
   }
-  return pdl_launch(scan_tc_kernel<NT, LOCAL>, dim3((unsigned)units), kTcThreads, smem, s, tp);
+  tp.units = (int)units;
+  return pdl_launch(scan_tc_kernel<NT, LOCAL>, dim3((unsigned)(units < num_sms ? units : num_sms)), kTcThreads, smem, s, tp);
 }
 
 template <int NT>
-cudaError_t launch_scan_nt(const ScanTcParams& tp, cudaStream_t s) {
+cudaError_t launch_scan_nt(ScanTcParams& tp, int num_sms, cudaStream_t s) {
   const ScanParams& p = tp.s;
   const int64_t heads = (int64_t)p.H * ((p.P + kPT - 1) / kPT);
-  if (!p.seg_tokens) return launch_tc<NT, false>(tp, p.pk.n_seqs * heads, s);
-  cudaError_t e = launch_tc<NT, true>(tp, p.max_segs * heads, s);
+  if (!p.seg_tokens) return launch_tc<NT, false>(tp, p.pk.n_seqs * heads, num_sms, s);
+  cudaError_t e = launch_tc<NT, true>(tp, p.max_segs * heads, num_sms, s);
   if (e != cudaSuccess) return e;
   e = pdl_launch(scan_carry_kernel, dim3((unsigned)((int64_t)p.pk.n_seqs * p.H), (p.P * p.N / 4 + 255) / 256), 256, 0, s,
                  tp.s);
-  return e != cudaSuccess ? e : launch_tc<NT, false>(tp, p.max_segs * heads, s);
+  return e != cudaSuccess ? e : launch_tc<NT, false>(tp, p.max_segs * heads, num_sms, s);
 }
 
 }  // namespace
@@ -752,14 +856,14 @@ ScanSplit scan_split(int64_t tokens, int32_t n_seqs, int64_t max_len, int H, int
   return {(int32_t)(seg * kChunk), (int32_t)(tokens / (seg * kChunk) + n_seqs)};
 }
 
-cudaError_t launch_scan_tc(const ScanParams& p, cudaStream_t s) {
+cudaError_t launch_scan_tc(const ScanParams& p, int num_sms, cudaStream_t s) {
   ScanTcParams tp;
   tp.s = p;
   tp.wide_y = p.P % 16 == 0 && reinterpret_cast<uintptr_t>(p.y) % 32 == 0;
   if (!tile_map(&tp.q, p.q, p.pk.tokens, p.G, p.N) || !tile_map(&tp.k, p.k, p.pk.tokens, p.G, p.N) ||
       !tile_map(&tp.v, p.v, p.pk.tokens, p.H, p.P))
     return cudaErrorInvalidValue;
-  return p.N > 64 ? launch_scan_nt<128>(tp, s) : launch_scan_nt<64>(tp, s);
+  return p.N > 64 ? launch_scan_nt<128>(tp, num_sms, s) : launch_scan_nt<64>(tp, num_sms, s);
 }
 
 }  // namespace replay

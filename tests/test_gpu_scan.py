@@ -39,6 +39,9 @@ CASES = [
     Case("f32_n64_p40", 2, 1, 40, 64, (33, 131), "f32"),
     Case("many_short", 4, 2, 64, 128, tuple(1 + i % 5 for i in range(70)), "bf16", resume="some", rows=80),
     Case("long", 2, 1, 64, 128, (5003,), "bf16", resume="all"),
+    # more units than SMs: a block takes several, of sorted and of unsorted sequences
+    Case("many_units", 16, 4, 64, 128, tuple(37 * i % 300 for i in range(40)), "bf16", resume="some", rows=41),
+    Case("many_units_n32", 8, 8, 80, 32, tuple(1 + 53 * i % 290 for i in range(70)), "bf16", resume="some", rows=75),
     Case("long_several", 2, 2, 128, 128, (2900, 0, 1, 2561, 256, 129), "bf16", resume="some", rows=9, lead=4, tail=9),
     Case("long_n64", 3, 1, 24, 64, (1, 2000, 3333), "bf16", resume="some", rows=3),
     Case("long_f32", 1, 1, 32, 64, (3001, 40), "f32"),
