@@ -21,14 +21,14 @@ namespace {
 constexpr int kChunk = 128;
 constexpr int kPT = 64;        // state rows of one block
 constexpr int kSplitSms = 148;  // the SMs that a split aims to fill
-constexpr int kTcThreads = 640;
-// Five warpgroups: 0 and 1 (rows of C, halves of the columns: P and the outputs), 2 (tokens:
-// decays and U), 3 (columns of the state), 4 (TMA, MMA and the plan). At 96 registers a thread at
-// launch, 2 and 4 give up what the state needs: (2 x 96 + 80 + 128 + 80) x 128 <= 5 x 96 x 128.
-constexpr int kWarpU = 8, kWarpS = 12, kWarpTma = 16, kWarpMmaQ = 17, kWarpMmaU = 18, kWarpPlan = 19;
-constexpr int kRegsLaunch = 96, kRegsTokens = 80, kRegsState = 128, kRegsCopy = 80;
-static_assert(2 * kRegsLaunch + kRegsTokens + kRegsState + kRegsCopy <= 5 * kRegsLaunch, "registers moved, not made");
-constexpr int kSlots = 3;  // chunks whose decays are held
+constexpr int kTcThreads = 896;
+// Seven warpgroups: 0 and 1 (rows of C: P and the outputs), 2 and 3 (tokens: decays and U),
+// 4 and 5 (columns of the state), each pair sharing the work by columns, and 6 (plan, TMA
+// and MMA). At 72 registers a thread at launch, 2, 3 and 6 give up what the state needs.
+constexpr int kWarpU = 8, kWarpS = 16, kWarpTma = 24, kWarpMmaQ = 25, kWarpMmaU = 26, kWarpPlan = 27;
+constexpr int kRegsLaunch = 72, kRegsTokens = 64, kRegsState = 88, kRegsCopy = 56;
+static_assert(2 * (kRegsLaunch + kRegsTokens + kRegsState) + kRegsCopy <= 7 * kRegsLaunch, "registers moved, not made");
+constexpr int kSlots = 5;  // chunks whose decays are held: who writes one knows that the fifth before it is done with
 
 struct alignas(64) ScanTcParams {
   CUtensorMap q, k, v;
@@ -39,6 +39,7 @@ struct alignas(64) ScanTcParams {
 
 // Tensor memory columns. P lies over C: the two BF16 parts of 16 columns of P take the 16
 // columns that held C's.
+// (LOCAL: two of dS alone).
 constexpr uint32_t kColC = 0, kColY1 = 128, kColY2 = 192, kColDS = 320;
 
 // A block's next unit: tokens [begin, begin + len) of one sequence, 64 state rows from p0 of
@@ -51,7 +52,7 @@ constexpr int kSortSeqs = 64;  // up to as many sequences are taken longest firs
 
 struct TcBars {
   uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t c_full, p_full, y_full, y_free, u_full, ds_full, ds_free, s_full, da_full[kSlots], drain[2];
+  uint64_t c_full, p_full, y_full, y_free, u_full[2], ds_full[2], ds_free[2], s_full, da_full[kSlots], drain[2];
   uint64_t unit_full[2], unit_empty[2];
   uint32_t tmem, abort;
   Unit unit[2];
@@ -66,13 +67,14 @@ struct alignas(16) Decays {
   int bad;            // the chunk holds a v that is not finite
 };
 
-template <int NT>
+template <int NT, bool LOCAL>
 struct TcLayout {  // bytes from the 1024-byte aligned base
   static constexpr int kTile = kChunk * 128;  // 128 rows of 64 BF16
   static constexpr int kQK = NT / 64 * kTile;
-  static constexpr int kSop = NT * 128;  // one part of the state operand: NT rows of 64 BF16
-  static constexpr int q = 0, k = kQK, v = k + 2 * kQK, u = v + 2 * kTile, s = u + 3 * kTile;
-  static constexpr int dec = s + 2 * kSop;
+  static constexpr int kSop = NT * 128;     // one part of the state operand: NT rows of 64 BF16
+  static constexpr int kU = LOCAL ? 2 : 1;  // buffers of U and of dS
+  static constexpr int q = 0, k = LOCAL ? 0 : kQK, v = k + 2 * kQK, u = v + 2 * kTile, s = u + kU * 3 * kTile;
+  static constexpr int dec = s + (LOCAL ? 0 : 2 * kSop);
   static constexpr int bars = dec + kSlots * (int)sizeof(Decays);
   static_assert(dec % 16 == 0 && bars % 8 == 0, "vector reads of the decays, 8-byte barriers");
   static constexpr int bytes = bars + (int)sizeof(TcBars) + 1024;
@@ -138,7 +140,7 @@ __device__ __forceinline__ bool find_segment(const Packed& pk, int seg_tokens, i
 // LOCAL: only the segments' own states, from zero, for those with a segment behind them.
 template <int NT, bool LOCAL>
 __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_constant__ ScanTcParams tp) {
-  using Lay = TcLayout<NT>;
+  using Lay = TcLayout<NT, LOCAL>;
   constexpr int kTile = Lay::kTile;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -154,15 +156,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
     mbar_init(&bars->q_full, 1), mbar_init(&bars->q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->k_full[i], 1), mbar_init(&bars->k_empty[i], LOCAL ? 1 : 2);
-      mbar_init(&bars->v_full[i], 1), mbar_init(&bars->v_empty[i], LOCAL ? 128 : 1);
+      mbar_init(&bars->v_full[i], 1), mbar_init(&bars->v_empty[i], LOCAL ? 256 : 1);
     }
     mbar_init(&bars->c_full, 1), mbar_init(&bars->p_full, 256);
     mbar_init(&bars->y_full, 1), mbar_init(&bars->y_free, 256);
-    mbar_init(&bars->u_full, 128), mbar_init(&bars->s_full, 128);
-    mbar_init(&bars->ds_full, 1), mbar_init(&bars->ds_free, 128);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars->u_full[i], 256);
+    mbar_init(&bars->s_full, 256);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars->ds_full[i], 1), mbar_init(&bars->ds_free[i], 256);
     for (int i = 0; i < kSlots; ++i) mbar_init(&bars->da_full[i], 128);
     mbar_init(&bars->drain[0], 1), mbar_init(&bars->drain[1], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&bars->unit_full[i], 1), mbar_init(&bars->unit_empty[i], LOCAL ? 10 : 19);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars->unit_full[i], 1), mbar_init(&bars->unit_empty[i], LOCAL ? 18 : 27);
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -213,6 +216,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
     if (lane == 0) mbar_arrive(&bars->unit_empty[k & 1]);
     return uniform(u.len < 0 ? -1 : (u.len + kChunk - 1) / kChunk);
   };
+  auto ds_col = [](int n) { return LOCAL ? (uint32_t)(n & 1) * 256 : kColDS; };
   // Every role walks the block's units and their chunks; n counts the chunks, over all units,
   // and gives the phases of the barriers.
 
@@ -237,11 +241,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
       int k = 0;
       bool more = true;
 #pragma unroll 1
-      for (int id = blockIdx.x; more; id += gridDim.x) {
+      for (int round = 0; more; ++round) {
+        // after the first round the blocks take units in turned order: long ones go with short ones
+        const int id = round * gridDim.x + (round == 0 ? blockIdx.x : gridDim.x - 1 - blockIdx.x);
         Unit u;
         u.len = -1;
-        more = id < tp.units;
+        more = round * (int64_t)gridDim.x < tp.units;
         if (more) {
+          if (id >= tp.units) continue;
           int s = id / heads, seg = 0, segs = 1;
           if (p.seg_tokens && !find_segment(p.pk, p.seg_tokens, s, s, seg, segs)) continue;
           if (LOCAL && seg == segs - 1) continue;
@@ -259,6 +266,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
           u.id = id;
           u.from = LOCAL ? 0 : segs > 1 ? 2 : p.pk.resume && p.pk.resume[s] ? 1 : 0;
           u.to = LOCAL ? 2 : seg == segs - 1 ? 1 : 0;
+          if (u.from && lane == 0)  // the state that it starts from into L2
+            prefetch_l2(u.from == 2 ? p.seg_state + (size_t)id * kPT * p.N
+                                    : p.S + (((size_t)u.row * p.H + u.h) * p.P + u.p0) * p.N,
+                        (p.P - u.p0 < kPT ? p.P - u.p0 : kPT) * p.N * 4);
         }
         if (k >= 2 && !wait_warp(&bars->unit_empty[k & 1], (k >> 1) - 1)) break;
         if (lane == 0) {
@@ -302,6 +313,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
         }
         mbar_arrive_expect_tx(&bars->v_full[b], kTile);
         tma_load3(smem + Lay::v + b * kTile, &tp.v, u.p0, u.h, t, &bars->v_full[b]);
+        if (c + 1 < chunks) {  // the next tiles' loads start late too
+          tma_prefetch3(&tp.v, u.p0, u.h, t + kChunk);
+#pragma unroll 1
+          for (int i = 0; i < NT / 64; ++i) tma_prefetch3(&tp.k, 64 * i, u.g, t + kChunk);
+        }
         ++n, ++c;
         tq = t, gq = u.g;
       }
@@ -367,14 +383,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
           const int b = n & 1;
           const uint64_t dk = smem_desc(smem_u32(smem + Lay::k + b * Lay::kQK), kTile);
           const uint64_t dv = smem_desc(smem_u32(smem + Lay::v + b * kTile), 16);
-          // dS = K^T U, the three parts side by side
-          if (!(ok = wait2_warp(&bars->u_full, n, &bars->k_full[b], n >> 1))) break;
-          if (n >= 1 && !(ok = wait_warp(&bars->ds_free, n - 1))) break;
+          // dS = K^T U, the three parts side by side, behind C, which the rows wait for
+          if (!(ok = wait2_warp(&bars->u_full[n % Lay::kU], n / Lay::kU, &bars->k_full[b], n >> 1))) break;
+          if (n >= Lay::kU && !(ok = wait_warp(&bars->ds_free[n % Lay::kU], n / Lay::kU - 1))) break;
+          if (!LOCAL && !(ok = wait_warp(&bars->c_full, n))) break;
           tc_fence_after();
           if (elect_lane()) {
 #pragma unroll 2
-            for (int i = 0; i < kChunk / 16; ++i) mma_ss(tmem + kColDS, dk + i * 128, du + i * 128, kDS, i > 0);
-            mma_commit(&bars->ds_full);
+            for (int i = 0; i < kChunk / 16; ++i) mma_ss(tmem + ds_col(n), dk + i * 128, du + (n % Lay::kU * 3 * kTile >> 4) + i * 128, kDS, i > 0);
+            mma_commit(&bars->ds_full[n % Lay::kU]);
             mma_commit(&bars->k_empty[b]);
           }
           if (LOCAL) continue;
@@ -524,7 +541,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
   } else if (warp < kWarpS) {
     // ------------------------------------------------------------ decays and U: token j of the chunk
     regs_down<kRegsTokens>();
-    const int j = threadIdx.x - 32 * kWarpU, w4 = warp - kWarpU;
+    const int j = (threadIdx.x - 32 * kWarpU) & 127, w4 = warp & 3, half = (warp - kWarpU) >> 2;
     float a = 1.f, dt = 0.f;
     Unit u;
     int n = 0, chunks;
@@ -538,46 +555,50 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
         a = in ? p.a[(size_t)t * p.H + u.h] : 1.f;
         dt = in ? p.dt[(size_t)t * p.H + u.h] : 0.f;
       };
-      load_da(0);
+      if (half == 0) load_da(0);
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c, ++n) {
         const int b = n & 1;
         Decays& d = dec[n % kSlots];
         const int len = u.len - c * kChunk < kChunk ? u.len - c * kChunk : kChunk;
-        // products of the decays up to and after this token, in its block and then over the chunk
-        float pre = a, suf = a;
+        if (half == 0) {
+          // products of the decays up to and after this token, in its block and then over the chunk
+          float pre = a, suf = a;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const float e = __shfl_up_sync(0xffffffffu, pre, off), f = __shfl_down_sync(0xffffffffu, suf, off);
-          if (lane >= off) pre *= e;
-          if (lane + off < 32) suf *= f;
+          for (int off = 1; off < 32; off <<= 1) {
+            const float e = __shfl_up_sync(0xffffffffu, pre, off), f = __shfl_down_sync(0xffffffffu, suf, off);
+            if (lane >= off) pre *= e;
+            if (lane + off < 32) suf *= f;
+          }
+          suf = __shfl_down_sync(0xffffffffu, suf, 1);
+          if (lane == 31) suf = 1.f;
+          if (lane == 31) d.total[w4] = pre;
+          if (j == 0) d.bad = 0;
+          d.pre[j] = pre;
+          d.g[j] = dt * suf;
+          d.da[j].y = dt;
+          if (j > 0) d.da[j - 1].x = a;
+          if (j == kChunk - 1) d.da[j].x = 1.f;
+          mbar_arrive(&bars->da_full[n % kSlots]);
+          load_da(c + 1);
         }
-        suf = __shfl_down_sync(0xffffffffu, suf, 1);
-        if (lane == 31) suf = 1.f;
-        if (lane == 31) d.total[w4] = pre;
-        if (j == 0) d.bad = 0;
-        d.pre[j] = pre;
-        d.g[j] = dt * suf;
-        d.da[j].y = dt;
-        if (j > 0) d.da[j - 1].x = a;
-        if (j == kChunk - 1) d.da[j].x = 1.f;
-        mbar_arrive(&bars->da_full[n % kSlots]);
         if (!(ok = wait_warp(&bars->da_full[n % kSlots], n / kSlots))) break;
-        float wj = dt * suf;
+        float wj = d.g[j];
 #pragma unroll
         for (int x = 1; x < 4; ++x)
           if (x > w4) wj *= d.total[x];
-        load_da(c + 1);
 
         if (!(ok = wait_warp(&bars->v_full[b], n >> 1))) break;
-        if (n >= 1 && !(ok = wait_warp(&bars->ds_full, n - 1))) break;  // U's last values have been read
+        // the buffer's last values have been read
+        if (n >= Lay::kU && !(ok = wait_warp(&bars->ds_full[n % Lay::kU], n / Lay::kU - 1))) break;
         uint8_t* vrow = smem + Lay::v + b * kTile + j * 128;
-        uint8_t* urow = smem + Lay::u + j * 128;
+        uint8_t* urow = smem + Lay::u + n % Lay::kU * 3 * kTile + j * 128;
         if (len < kChunk && !(ok = wait_warp(&bars->k_full[b], n >> 1))) break;
         if (j >= len) {
           // another sequence's tokens: zeros in v and k (0 times its NaN would be NaN)
-          for (int x = 0; x < 8; ++x) *reinterpret_cast<uint4*>(vrow + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
-          for (int i = 0; i < NT / 64; ++i)
+          for (int x = 4 * half; x < 4 * half + 4; ++x)
+            *reinterpret_cast<uint4*>(vrow + ((x ^ (j & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+          for (int i = half; i < NT / 64; i += 2)
             for (int x = 0; x < 8; ++x)
               *reinterpret_cast<uint4*>(smem + Lay::k + b * Lay::kQK + i * kTile + j * 128 + 16 * x) =
                   make_uint4(0u, 0u, 0u, 0u);
@@ -585,7 +606,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
         const f32x2 ww = pair(wj, wj);
         f32x2 check[2] = {0, 0};  // 0 times what is not finite is NaN
 #pragma unroll 2
-        for (int x = 0; x < 8; ++x) {
+        for (int x = 4 * half; x < 4 * half + 4; ++x) {
           const int at = (x ^ (j & 7)) << 4;
           const uint4 vu = *reinterpret_cast<const uint4*>(vrow + at);
           float f[8];
@@ -609,23 +630,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
         if (!LOCAL && c0 + c1 != 0.f) {
           // what is not finite must not meet the zeros of the earlier tokens' rows of P
 #pragma unroll 1
-          for (int x = 0; x < 64; ++x) {
-            uint16_t* e = reinterpret_cast<uint16_t*>(vrow) + x;
+          for (int x = 32 * half; x < 32 * half + 32; ++x) {
+            uint16_t* e = reinterpret_cast<uint16_t*>(vrow + (((x >> 3) ^ (j & 7)) << 4)) + (x & 7);
             if ((*e & 0x7F80) == 0x7F80) *e = 0;
           }
           d.bad = 1;
         }
         fence_async_smem();
-        mbar_arrive(&bars->u_full);
+        mbar_arrive(&bars->u_full[n % Lay::kU]);
         if (LOCAL) mbar_arrive(&bars->v_empty[b]);
       }
     }
   } else if (warp < kWarpTma) {
     // ------------------------------------------------------------ the state: column n
     regs_up<kRegsState>();
-    const int sn = threadIdx.x - 32 * kWarpS, w4 = warp - kWarpS;  // column n
+    const int sn = (threadIdx.x - 32 * kWarpS) & 127, w4 = warp & 3, half = (warp - kWarpS) >> 2;  // column n, half of p
     const uint32_t tl = tmem + ((uint32_t)(w4 * 32) << 16);
-    f32x2 S[kPT / 2];
+    f32x2 S[kPT / 4];
     // 16 rows p of the state's two BF16 parts as an operand: row n, chunk x at x ^ (n % 8)
     uint8_t* dst = smem + Lay::s + sn * 128;
     auto put_state = [&](int part) {
@@ -638,7 +659,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
           hi[e] = take_part(f);
           lo[e] = last_part(f);
         }
-        uint8_t* at = dst + ((x ^ (sn & 7)) << 4);
+        uint8_t* at = dst + (((4 * half + x) ^ (sn & 7)) << 4);
         *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(at + Lay::kSop) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
@@ -649,18 +670,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
 #pragma unroll 1
     for (int k = 0; ok && (chunks = take_unit_warp(u, k)) >= 0; ++k) {
       // rows p of the state that it starts from: the caller's, a segment's, or zero
-      float* Sg = p.S + (((size_t)u.row * p.H + u.h) * p.P + u.p0) * p.N + sn;
-      float* Eg = p.seg_state + (size_t)u.id * kPT * p.N + sn;
-      const int rows = sn < p.N ? p.P - u.p0 : 0;  // P is a multiple of 8
+      float* Sg = p.S + (((size_t)u.row * p.H + u.h) * p.P + u.p0 + 32 * half) * p.N + sn;
+      float* Eg = p.seg_state + ((size_t)u.id * kPT + 32 * half) * p.N + sn;
+      const int rows = sn < p.N ? p.P - u.p0 - 32 * half : 0;  // P is a multiple of 8
       const float* from = u.from == 2 ? Eg : Sg;
 #pragma unroll
-      for (int e = 0; e < kPT; e += 2)
+      for (int e = 0; e < kPT / 2; e += 2)
         S[e / 2] = u.from && e < rows ? pair(from[(size_t)e * p.N], from[(size_t)(e + 1) * p.N]) : 0;
       float decay = 1.f;
       if (!LOCAL && chunks > 0) {  // the last chunk's Y2 has read the operand
         if (sn < NT) {
 #pragma unroll
-          for (int part = 0; part < 4; ++part) put_state(part);
+          for (int part = 0; part < 2; ++part) put_state(part);
         }
         fence_async_smem();
         mbar_arrive(&bars->s_full);
@@ -668,7 +689,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c, ++n) {
         // dS is there, and Y2 has read the state's operand
-        if (!(ok = LOCAL ? wait_warp(&bars->ds_full, n) : wait2_warp(&bars->ds_full, n, &bars->q_empty, n))) break;
+        if (!(ok = LOCAL ? wait_warp(&bars->ds_full[n % Lay::kU], n / Lay::kU) : wait2_warp(&bars->ds_full[0], n, &bars->q_empty, n))) break;
         tc_fence_after();
         const float* tot = dec[n % kSlots].total;
         const float all = (tot[0] * tot[1]) * (tot[2] * tot[3]);
@@ -676,11 +697,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
         if (LOCAL) decay *= all;
         const bool put = !LOCAL && c + 1 < chunks;
 #pragma unroll
-        for (int part = 0; part < 4; ++part) {
+        for (int part = 0; part < 2; ++part) {
           uint32_t d1[16], d2[16], d3[16];
-          tmem_ld16(tl + kColDS + 16 * part, d1);
-          tmem_ld16(tl + kColDS + kPT + 16 * part, d2);
-          tmem_ld16(tl + kColDS + 2 * kPT + 16 * part, d3);
+          const uint32_t at = tl + ds_col(n) + 32 * half + 16 * part;
+          tmem_ld16(at, d1);
+          tmem_ld16(at + kPT, d2);
+          tmem_ld16(at + 2 * kPT, d3);
           tmem_wait_ld16(d1);
           tmem_wait_ld16(d2);
           tmem_wait_ld16(d3);
@@ -692,7 +714,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
           if (put && sn < NT) put_state(part);
         }
         tc_fence_before();
-        mbar_arrive(&bars->ds_free);
+        mbar_arrive(&bars->ds_free[n % Lay::kU]);
         if (put) {
           fence_async_smem();
           mbar_arrive(&bars->s_full);
@@ -701,7 +723,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
       if (!ok || !u.to) continue;
       float* to = u.to == 2 ? Eg : Sg;
 #pragma unroll
-      for (int e = 0; e < kPT; e += 2) {
+      for (int e = 0; e < kPT / 2; e += 2) {
         float s0, s1;
         unpair(S[e / 2], s0, s1);
         if (e < rows) {
@@ -709,8 +731,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
           to[(size_t)(e + 1) * p.N] = s1;
         }
       }
-      if (LOCAL && sn == 0) p.seg_decay[u.id] = decay;
-      if (!LOCAL && p.counts && u.h == 0 && u.p0 == 0 && sn == 0) p.counts[u.row] = 0;
+      if (LOCAL && sn == 0 && half == 0) p.seg_decay[u.id] = decay;
+      if (!LOCAL && p.counts && u.h == 0 && u.p0 == 0 && sn == 0 && half == 0) p.counts[u.row] = 0;
     }
   }
   __syncwarp();
@@ -808,7 +830,7 @@ bool tile_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int w
 
 template <int NT, bool LOCAL>
 cudaError_t launch_tc(ScanTcParams& tp, int64_t units, int num_sms, cudaStream_t s) {
-  constexpr int smem = TcLayout<NT>::bytes;
+  constexpr int smem = TcLayout<NT, LOCAL>::bytes;
   static bool configured[64] = {false};  // per device; setting it twice does no harm
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

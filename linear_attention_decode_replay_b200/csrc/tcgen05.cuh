@@ -134,6 +134,10 @@ __device__ __forceinline__ void tma_load3(void* dst, const CUtensorMap* map, int
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
+// `bytes` (a multiple of 16) from a 16-byte aligned address into L2
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
 // Tests a phase, suspending the thread for about a microsecond at most.
 constexpr int kPollLimit = 2000000;  // polls of one wait, ~2 s
 __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
