@@ -90,19 +90,30 @@ int check_scratch(const void* scratch, int64_t have, int64_t need) {
 }
 
 // The scratch of one scan: the segments' states, then their decays.
-bool on_tensor_cores(const replay_config& c, int64_t tokens) { return c.io == REPLAY_BF16 && tokens > 0; }
+// The serial kernel takes FP32 inputs, and BF16 sequences of few tokens, where the tensor
+// cores' chunks of 128 are mostly empty: a chunk of one head takes an SM about 6 us with its
+// state, a token of the serial kernel 0.27 us in each of a few blocks an SM (256 sequences of
+// the 64-head layer: 16 tokens each 443 against 672 us, 32 tokens 743 against 670 us).
+bool on_tensor_cores(const replay_config& c, int64_t tokens, int32_t n_seqs, int64_t max_len) {
+  if (c.io != REPLAY_BF16 || tokens == 0) return false;
+  constexpr int64_t kFew = 24;
+  if (tokens > kFew * n_seqs) return true;
+  const int64_t longest = max_len > 0 && max_len < tokens ? max_len : tokens;
+  const int64_t units = (int64_t)n_seqs * c.heads * ((c.P + 63) / 64);
+  return longest > kFew && longest * 148 > kFew * units;  // one of them is long, and the others hide it not
+}
 int64_t segment_units(const replay_config& c, const replay::ScanSplit& sp) {
   return (int64_t)sp.max_segs * c.heads * ((c.P + 63) / 64);
 }
 int64_t scan_scratch(const replay_config& c, int64_t tokens, int32_t n_seqs, int64_t max_len) {
-  if (!on_tensor_cores(c, tokens)) return 0;
+  if (!on_tensor_cores(c, tokens, n_seqs, max_len)) return 0;
   const replay::ScanSplit sp = replay::scan_split(tokens, n_seqs, max_len, c.heads, c.P);
   const int64_t units = sp.seg_tokens ? segment_units(c, sp) : 0;
   return round256(units * 64 * c.N * 4) + round256(units * 4);
 }
 
 int launch_scan(ScanParams& p, const replay_config& c, int64_t max_len, void* scratch, cudaStream_t s) {
-  if (!on_tensor_cores(c, p.pk.tokens)) return launched(replay::launch_scan_serial(p, c.io, s));
+  if (!on_tensor_cores(c, p.pk.tokens, p.pk.n_seqs, max_len)) return launched(replay::launch_scan_serial(p, c.io, s));
   const replay::ScanSplit sp = replay::scan_split(p.pk.tokens, p.pk.n_seqs, max_len, c.heads, c.P);
   p.seg_tokens = sp.seg_tokens, p.max_segs = sp.max_segs;
   p.seg_state = static_cast<float*>(scratch);

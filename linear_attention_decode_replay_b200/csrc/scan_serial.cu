@@ -2,17 +2,25 @@
 //   S <- a_t S + Delta_t v_t k_t^T,   y_t = S q_t.
 // A block holds a block of state rows of one head of one sequence in registers and walks
 // the sequence's tokens; a thread holds kRows rows of kCols columns. All arithmetic is
-// FP32. It serves every size and type; 3 P N FMAs per token and head bound it.
+// FP32, as packed pairs (three instructions for two elements a token). It serves every size
+// and type; the packed FMAs, 3 P N / 2 a token and head, bound it where there are enough
+// blocks, and a token's chain of them (with a share of the sums over the lanes of a row)
+// where there are few.
 #include "layer_device.cuh"
+#include "tcgen05.cuh"
 
 namespace replay {
 
 namespace {
 
 constexpr int kSerialThreads = 128;
-constexpr int kSerialTokens = 16;  // tokens staged in shared memory together
+constexpr int kBatch = 8;          // tokens whose sums over a row's lanes are taken together
 constexpr int kRows = 2, kCols = 16;
 
+template <int N>
+constexpr int serial_tokens() {  // tokens staged in shared memory together
+  return N == 16 ? 8 : 16;
+}
 template <int N>
 constexpr int serial_rows() {  // state rows of one block
   return kSerialThreads / (N / kCols) * kRows;
@@ -24,10 +32,10 @@ template <typename IO, int N>
 __global__ void __launch_bounds__(kSerialThreads) scan_serial_kernel(const __grid_constant__ ScanParams p) {
   constexpr int TPR = N / kCols;  // lanes that share a row
   constexpr int RB = serial_rows<N>();
-  constexpr int TC = kSerialTokens, V = Vec<IO>::n;
-  __shared__ __align__(16) float sk[TC][N], sq[TC][N], sv[TC][RB];
-  __shared__ float2 sda[TC];  // Delta, a
-  __shared__ __align__(16) float sy[TC][RB];
+  constexpr int TC = serial_tokens<N>(), V = Vec<IO>::n;
+  // two stages: one is filled and its outputs drained while the other is computed
+  __shared__ __align__(16) float sk[2][TC][N], sq[2][TC][N], sv[2][TC][RB], sy[2][TC][RB];
+  __shared__ float2 sda[2][TC];  // Delta, a
   pdl_enter();
   const int row_blocks = (p.P + RB - 1) / RB;
   const int s = blockIdx.x / (p.H * row_blocks);
@@ -42,87 +50,124 @@ __global__ void __launch_bounds__(kSerialThreads) scan_serial_kernel(const __gri
   const int lane = threadIdx.x % TPR;  // columns 4 (lane + TPR i) + 0..3
   const int r0 = threadIdx.x / TPR * kRows;
   float* Sg = p.S + (((size_t)row * p.H + h) * p.P + p0) * N;
-  float S[kRows][kCols];
+  f32x2 S[kRows][kCols / 2];
   const bool res = p.pk.resume && p.pk.resume[s];
 #pragma unroll
   for (int r = 0; r < kRows; ++r)
 #pragma unroll
     for (int i = 0; i < kCols / 4; ++i) {
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (res && r0 + r < rows) x = *reinterpret_cast<const float4*>(Sg + (size_t)(r0 + r) * N + 4 * (lane + TPR * i));
-      S[r][4 * i] = x.x, S[r][4 * i + 1] = x.y, S[r][4 * i + 2] = x.z, S[r][4 * i + 3] = x.w;
+      ulonglong2 x = make_ulonglong2(0, 0);
+      if (res && r0 + r < rows)
+        x = *reinterpret_cast<const ulonglong2*>(Sg + (size_t)(r0 + r) * N + 4 * (lane + TPR * i));
+      S[r][2 * i] = x.x, S[r][2 * i + 1] = x.y;
     }
 
-  const IO* q = static_cast<const IO*>(p.q);
-  const IO* k = static_cast<const IO*>(p.k);
-  const IO* v = static_cast<const IO*>(p.v);
-  for (int64_t t0 = begin; t0 < end; t0 += TC) {
-    const int n = end - t0 < TC ? (int)(end - t0) : TC;
-    __syncthreads();  // the last tokens' reads are done
-    for (int i = threadIdx.x; i < n * (N / V); i += kSerialThreads) {
-      const int t = i / (N / V), c = i % (N / V) * V;
-      const size_t at = ((size_t)(t0 + t) * p.G + g) * N + c;
-      Vec<IO>::unpack(*reinterpret_cast<const uint4*>(k + at), &sk[t][c]);
-      Vec<IO>::unpack(*reinterpret_cast<const uint4*>(q + at), &sq[t][c]);
-    }
-    const int vr = rows / V;
-    for (int i = threadIdx.x; i < n * vr; i += kSerialThreads) {
-      const int t = i / vr, c = i % vr * V;
-      Vec<IO>::unpack(*reinterpret_cast<const uint4*>(v + ((size_t)(t0 + t) * p.H + h) * p.P + p0 + c), &sv[t][c]);
-    }
-    if (threadIdx.x < n) {
-      const size_t at = (size_t)(t0 + threadIdx.x) * p.H + h;
-      sda[threadIdx.x] = make_float2(p.dt[at], p.a[at]);
-    }
-    __syncthreads();
-    if ((int)(threadIdx.x & ~31u) / TPR * kRows < rows) {  // the warp holds a row of the head
-      for (int t = 0; t < n; ++t) {
-        const float2 da = sda[t];
-        float y[kRows], w[kRows];
+  // the next stage's values on their way: vectors of k and q, of v, and one token's Delta, a
+  constexpr int KV = (TC * N / V + kSerialThreads - 1) / kSerialThreads;
+  constexpr int VV = (TC * RB / V + kSerialThreads - 1) / kSerialThreads;
+  const IO* q = static_cast<const IO*>(p.q) + (size_t)g * N;
+  const IO* k = static_cast<const IO*>(p.k) + (size_t)g * N;
+  const IO* v = static_cast<const IO*>(p.v) + (size_t)h * p.P + p0;
+  uint4 fk[KV], fq[KV], fv[VV];
+  float2 fda;
+  auto fetch = [&](int64_t t0) {  // past the sequence: zeros, and no decay
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-          y[r] = 0.f;
-          w[r] = da.x * sv[t][r0 + r];
-        }
+    for (int u = 0; u < KV; ++u) {
+      const int i = u * kSerialThreads + threadIdx.x, t = i / (N / V), c = i % (N / V) * V;
+      const bool in = t < TC && t0 + t < end;
+      fk[u] = in ? *reinterpret_cast<const uint4*>(k + (size_t)(t0 + t) * p.G * N + c) : Vec<IO>::zero();
+      fq[u] = in ? *reinterpret_cast<const uint4*>(q + (size_t)(t0 + t) * p.G * N + c) : Vec<IO>::zero();
+    }
+#pragma unroll
+    for (int u = 0; u < VV; ++u) {
+      const int i = u * kSerialThreads + threadIdx.x, t = i / (RB / V), c = i % (RB / V) * V;
+      const bool in = t < TC && t0 + t < end && c < rows;
+      fv[u] = in ? *reinterpret_cast<const uint4*>(v + (size_t)(t0 + t) * p.H * p.P + c) : Vec<IO>::zero();
+    }
+    fda = make_float2(0.f, 1.f);
+    if (threadIdx.x < TC && t0 + threadIdx.x < end) {
+      const size_t at = (size_t)(t0 + threadIdx.x) * p.H + h;
+      fda = make_float2(p.dt[at], p.a[at]);
+    }
+  };
+  auto store_y = [&](int64_t t0, int b) {
+    for (int i = threadIdx.x; i < TC * (RB / V); i += kSerialThreads) {
+      const int t = i / (RB / V), c = i % (RB / V) * V;
+      if (t0 + t < end && c < rows)
+        *reinterpret_cast<uint4*>(static_cast<IO*>(p.y) + ((size_t)(t0 + t) * p.H + h) * p.P + p0 + c) =
+            Vec<IO>::pack(&sy[b][t][c]);
+    }
+  };
+
+  int b = 0;
+  if (begin < end) fetch(begin);
+  for (int64_t t0 = begin; t0 < end; t0 += TC, b ^= 1) {
+#pragma unroll
+    for (int u = 0; u < KV; ++u) {
+      const int i = u * kSerialThreads + threadIdx.x, t = i / (N / V), c = i % (N / V) * V;
+      if (t < TC) {
+        Vec<IO>::unpack(fk[u], &sk[b][t][c]);
+        Vec<IO>::unpack(fq[u], &sq[b][t][c]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < VV; ++u) {
+      const int i = u * kSerialThreads + threadIdx.x, t = i / (RB / V), c = i % (RB / V) * V;
+      if (t < TC) Vec<IO>::unpack(fv[u], &sv[b][t][c]);
+    }
+    if (threadIdx.x < TC) sda[b][threadIdx.x] = fda;
+    __syncthreads();  // this stage is there; the last one's outputs are, and its inputs are read
+    if (t0 + TC < end) fetch(t0 + TC);
+    if (t0 > begin) store_y(t0 - TC, b ^ 1);
+    if ((int)(threadIdx.x & ~31u) / TPR * kRows >= rows) continue;  // the warp holds no row of the head
+#pragma unroll 1
+    for (int tb = 0; tb < TC && t0 + tb < end; tb += kBatch) {
+      float y[kBatch * kRows];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const float2 da = sda[b][tb + u];
+        const float2 vv = *reinterpret_cast<const float2*>(&sv[b][tb + u][r0]);
+        const f32x2 a2 = pair(da.y, da.y);
+        const f32x2 w2[kRows] = {pair(da.x * vv.x, da.x * vv.x), pair(da.x * vv.y, da.x * vv.y)};
+        f32x2 y2[kRows] = {0, 0};
 #pragma unroll
         for (int i = 0; i < kCols / 4; ++i) {
-          const float4 kk = *reinterpret_cast<const float4*>(&sk[t][4 * (lane + TPR * i)]);
-          const float4 qq = *reinterpret_cast<const float4*>(&sq[t][4 * (lane + TPR * i)]);
+          const ulonglong2 kk = *reinterpret_cast<const ulonglong2*>(&sk[b][tb + u][4 * (lane + TPR * i)]);
+          const ulonglong2 qq = *reinterpret_cast<const ulonglong2*>(&sq[b][tb + u][4 * (lane + TPR * i)]);
 #pragma unroll
           for (int r = 0; r < kRows; ++r) {
-            float* x = &S[r][4 * i];
-            x[0] = fmaf(w[r], kk.x, da.y * x[0]);
-            x[1] = fmaf(w[r], kk.y, da.y * x[1]);
-            x[2] = fmaf(w[r], kk.z, da.y * x[2]);
-            x[3] = fmaf(w[r], kk.w, da.y * x[3]);
-            y[r] = fmaf(x[0], qq.x, y[r]);
-            y[r] = fmaf(x[1], qq.y, y[r]);
-            y[r] = fmaf(x[2], qq.z, y[r]);
-            y[r] = fmaf(x[3], qq.w, y[r]);
+            f32x2* x = &S[r][2 * i];
+            x[0] = fma2(w2[r], kk.x, mul2(a2, x[0]));
+            x[1] = fma2(w2[r], kk.y, mul2(a2, x[1]));
+            y2[r] = fma2(x[0], qq.x, y2[r]);
+            y2[r] = fma2(x[1], qq.y, y2[r]);
           }
         }
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
-#pragma unroll
-          for (int off = TPR / 2; off >= 1; off >>= 1) y[r] += __shfl_xor_sync(0xffffffffu, y[r], off);
-          if (lane == 0) sy[t][r0 + r] = y[r];
+          float lo, hi;
+          unpair(y2[r], lo, hi);
+          y[u * kRows + r] = lo + hi;
         }
       }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n * vr; i += kSerialThreads) {
-      const int t = i / vr, c = i % vr * V;
-      *reinterpret_cast<uint4*>(static_cast<IO*>(p.y) + ((size_t)(t0 + t) * p.H + h) * p.P + p0 + c) =
-          Vec<IO>::pack(&sy[t][c]);
+      // sums over the row's lanes, transposed: each lane ends with some tokens' rows
+      int base;
+      using Red = SegReduce<kBatch * kRows, TPR>;
+      Red::run(y, threadIdx.x & 31, base);
+#pragma unroll
+      for (int e = 0; e < Red::kHeld; ++e)
+        sy[b][tb + (base + e) / kRows][r0 + (base + e) % kRows] = y[e];
     }
   }
+  __syncthreads();
+  if (begin < end) store_y(begin + (end - begin - 1) / TC * TC, b ^ 1);
 #pragma unroll
   for (int r = 0; r < kRows; ++r)
 #pragma unroll
     for (int i = 0; i < kCols / 4; ++i)
       if (r0 + r < rows)
-        *reinterpret_cast<float4*>(Sg + (size_t)(r0 + r) * N + 4 * (lane + TPR * i)) =
-            make_float4(S[r][4 * i], S[r][4 * i + 1], S[r][4 * i + 2], S[r][4 * i + 3]);
+        *reinterpret_cast<ulonglong2*>(Sg + (size_t)(r0 + r) * N + 4 * (lane + TPR * i)) =
+            make_ulonglong2(S[r][2 * i], S[r][2 * i + 1]);
   if (p.counts && h == 0 && p0 == 0 && threadIdx.x == 0) p.counts[row] = 0;
 }
 
