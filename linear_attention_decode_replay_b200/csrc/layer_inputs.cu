@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(kThreadsIn, 6) prompt_inputs_kernel(const __gr
     const bool owner = s >= lo;
     if (owner && !(pk.cu[s] < t1 || last)) break;
     int64_t begin, end;
+    const bool res = owner && pk.resume && pk.resume[s];  // on its way with the bounds and the row
     if (!seq_bounds(pk, s, begin, end)) continue;
     const int64_t ta = owner ? begin : (t0 > begin + K ? t0 : begin + K);
     const int64_t to = !owner || t1 > begin + K ? t1 : begin + K;
@@ -140,12 +141,22 @@ __global__ void __launch_bounds__(kThreadsIn, 6) prompt_inputs_kernel(const __gr
       continue;
     }
     if (!on) continue;
+    const uint8_t* xt = x + (size_t)ta * xs;
+    uint8_t* yt = d.base + (size_t)ta * d.stride;
+    int left = (int)(tb - ta);
+    // two groups of U tokens: one in flight while the other is computed
+    Raw xu[2][U];
+    auto fetch = [&](Raw* g) {  // the next U tokens from xt on, as far as there are any
+#pragma unroll
+      for (int u = 0; u < U; ++u) g[u] = u < left ? __ldg(reinterpret_cast<const Raw*>(xt + u * xs)) : Vc::zero();
+      xt += U * xs;
+    };
+    fetch(xu[0]);
     float hist[K][V];
     if (owner) {
       Raw old[K];
       Raw* st = reinterpret_cast<Raw*>(static_cast<uint8_t*>(p.conv) + ((size_t)row * K * p.D + c0) * sizeof(IO));
       const size_t ss = (size_t)p.D / V;
-      const bool res = pk.resume && pk.resume[s];
 #pragma unroll
       for (int i = 0; i < K; ++i) {
         old[i] = res ? st[i * ss] : Vc::zero();
@@ -168,23 +179,12 @@ __global__ void __launch_bounds__(kThreadsIn, 6) prompt_inputs_kernel(const __gr
 #pragma unroll
       for (int i = 0; i < K; ++i) Vc::unpack(x_at(ta - K + i), hist[i]);
     }
-    const uint8_t* xt = x + (size_t)ta * xs;
-    uint8_t* yt = d.base + (size_t)ta * d.stride;
-    int left = (int)(tb - ta);
-    // two groups of U tokens: one in flight while the other is computed
-    Raw xu[2][U];
-    auto fetch = [&](Raw* g) {  // the next U tokens from xt on, as far as there are any
-#pragma unroll
-      for (int u = 0; u < U; ++u) g[u] = u < left ? __ldg(reinterpret_cast<const Raw*>(xt + u * xs)) : Vc::zero();
-      xt += U * xs;
-    };
     auto put = [&](const Raw* g, int n) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (u < n) *reinterpret_cast<Raw*>(yt + u * d.stride) = f.step(hist, g[u]);
       yt += U * d.stride;
     };
-    fetch(xu[0]);
     while (left > 0) {
       int n = left;
       left -= U;

@@ -14,12 +14,19 @@ namespace replay {
 namespace {
 
 constexpr int kSerialThreads = 128;
-constexpr int kBatch = 8;          // tokens whose sums over a row's lanes are taken together
 constexpr int kRows = 2, kCols = 16;
 
-template <int N>
-constexpr int serial_tokens() {  // tokens staged in shared memory together
-  return N == 16 ? 8 : 16;
+// Tokens staged in shared memory together, and tokens whose sums over a row's lanes are taken
+// together: short BF16 sequences want little staging and many blocks an SM (256 sequences of
+// one token: 209 us with 8 and 4, 305 us with 16 and 8), FP32 prompts few barriers and sums
+// (four of 500 tokens: 219 us with 16 and 8, 270 us with 8 and 4).
+template <typename IO, int N>
+constexpr int serial_tokens() {
+  return sizeof(IO) == 2 || N == 16 ? 8 : 16;
+}
+template <typename IO>
+constexpr int serial_batch() {
+  return sizeof(IO) == 2 ? 4 : 8;
 }
 template <int N>
 constexpr int serial_rows() {  // state rows of one block
@@ -29,10 +36,10 @@ constexpr int serial_rows() {  // state rows of one block
 }  // namespace
 
 template <typename IO, int N>
-__global__ void __launch_bounds__(kSerialThreads) scan_serial_kernel(const __grid_constant__ ScanParams p) {
+__global__ void __launch_bounds__(kSerialThreads, sizeof(IO) == 2 ? 4 : 1) scan_serial_kernel(const __grid_constant__ ScanParams p) {
   constexpr int TPR = N / kCols;  // lanes that share a row
   constexpr int RB = serial_rows<N>();
-  constexpr int TC = serial_tokens<N>(), V = Vec<IO>::n;
+  constexpr int TC = serial_tokens<IO, N>(), kBatch = serial_batch<IO>(), V = Vec<IO>::n;
   // two stages: one is filled and its outputs drained while the other is computed
   __shared__ __align__(16) float sk[2][TC][N], sq[2][TC][N], sv[2][TC][RB], sy[2][TC][RB];
   __shared__ float2 sda[2][TC];  // Delta, a
