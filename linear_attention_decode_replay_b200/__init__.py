@@ -266,9 +266,8 @@ def _input_outs(cfg, n, like, out, dev):
     """q, k, v, dt, a of n tokens, `out` checked or new tensors, and their addresses."""
     _, t, _, qs, vs, hs = cfg._layer
     if out is None:
-        q, k, v = like.new_empty((n, *qs)), like.new_empty((n, *qs)), like.new_empty((n, *vs))
-        dt = like.new_empty((n, *hs), dtype=torch.float32)
-        a = like.new_empty((n, *hs), dtype=torch.float32)
+        q, v, dt = like.new_empty((n, *qs)), like.new_empty((n, *vs)), like.new_empty((n, *hs), dtype=torch.float32)
+        k, a = torch.empty_like(q), torch.empty_like(dt)
         return (q, k, v, dt, a), (q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(), a.data_ptr())
     q, k, v, dt, a = out
     f32 = torch.float32

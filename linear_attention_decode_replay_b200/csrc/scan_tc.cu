@@ -525,15 +525,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
             if (left > 8) *reinterpret_cast<uint4*>(y + 16 * part + 8) = make_uint4(o[4], o[5], o[6], o[7]);
           }
         }
-        if (bad && t < end) {
+        if (bad) {
           // the products saw zeros in place of what is not finite in v: it reaches every later row
-          const uint16_t* v = static_cast<const uint16_t*>(p.v) + u.p0 + 32 * half;
+          const uint16_t* v = static_cast<const uint16_t*>(p.v) + (size_t)u.h * p.P + u.p0 + 32 * half;
 #pragma unroll 1
-          for (int j = 0; j <= i; ++j) {
-            const uint16_t* vj = v + ((size_t)(t - i + j) * p.H + u.h) * p.P;
+          for (int e = 0; e < 32 && u.p0 + 32 * half + e < p.P; ++e) {
+            int first = kChunk;
 #pragma unroll 1
-            for (int e = 0; e < 32 && u.p0 + 32 * half + e < p.P; ++e)
-              if ((vj[e] & 0x7F80) == 0x7F80) reinterpret_cast<uint16_t*>(y)[e] = 0x7FC0;
+            for (int r0 = 0; r0 < kChunk && first == kChunk; r0 += 32) {
+              const int64_t tr = t - i + r0 + lane;
+              const uint16_t x = tr < end ? v[(size_t)tr * p.H * p.P + e] : 0;
+              const unsigned hit = __ballot_sync(0xffffffffu, (x & 0x7F80) == 0x7F80);
+              if (hit) first = r0 + __ffs(hit) - 1;
+            }
+            if (t < end && first <= i) reinterpret_cast<uint16_t*>(y)[e] = 0x7FC0;
           }
         }
       }

@@ -138,8 +138,9 @@ __device__ __forceinline__ void tma_load3(void* dst, const CUtensorMap* map, int
 __device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
-// Tests a phase, suspending the thread for about a microsecond at most.
-constexpr int kPollLimit = 2000000;  // polls of one wait, ~2 s
+// Tests a phase, suspending the thread for 100 ns or so at most.
+constexpr int kPollLimit = 20000000;  // polls of one wait: up to 2 s (a look at the clock in the
+                                      // loop cost the scan 7 %, in registers and instructions)
 __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -147,7 +148,7 @@ __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(1000)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(100)
       : "memory");
   return ok != 0;
 }

@@ -136,6 +136,23 @@ def test_bad_values_reach_only_what_follows_them(io, bad, what):
     assert np.array_equal(np.isfinite(got[t:350, 0]), np.isfinite(want[t:350, 0]))
 
 
+def test_values_not_finite_everywhere_in_v():
+    """Many of them, in every column and chunk: each output that one reaches is not finite, and
+    no other changes."""
+    case = Case("nan_v", 2, 1, 64, 128, (300,), "bf16", seed=9)
+    ins = scan_inputs(case)
+    y0, S0, cu, seqs, resume = run(case, ins)
+    x = [t.clone() for t in ins]
+    g = torch.Generator().manual_seed(1)
+    first = torch.randint(0, 400, (case.H, case.P), generator=g)  # from this token on
+    bad = torch.arange(case.T)[:, None, None] >= first[None]
+    x[2][bad.cuda()] = float("nan")
+    y1, S1, *_ = run(case, x)
+    assert torch.equal(torch.isfinite(y1).cpu(), ~bad)
+    assert torch.equal(y1[~bad.cuda()], y0[~bad.cuda()])
+    assert torch.equal(torch.isfinite(S1[0]).all(-1).cpu(), first >= case.T)
+
+
 def test_padding_and_bad_ids_are_skipped():
     case = Case("ids", 2, 1, 32, 32, (10, 20, 30, 40, 50), "bf16", resume="all")
     q, k, v, dt, a, S = ins = scan_inputs(case)
