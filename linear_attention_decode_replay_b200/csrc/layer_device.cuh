@@ -9,6 +9,32 @@ namespace replay {
 
 constexpr int32_t kErrSeqs = 1 << 4;  // a bad or repeated row id, or sequence bounds out of order
 
+// Blackwell's packed FP32: two products, sums or FMAs an instruction, each rounded to nearest
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(f32x2 x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // A vector of inputs, 16 bytes: 4 floats or 8 BF16; or 4 BF16 in 8 bytes.
 __device__ __forceinline__ uint32_t bf16_pack2(float lo, float hi) {
   const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
@@ -76,6 +102,21 @@ __device__ __forceinline__ float silu(float x) {
     return x * r;
   }
   return __fdividef(x, 1.f + expf(-x));
+}
+template <typename IO>
+__device__ __forceinline__ f32x2 silu2(f32x2 x) {
+  float a, b;
+  if constexpr (sizeof(IO) == 2) {
+    unpair(mul2(x, pair(-1.4426950408889634f, -1.4426950408889634f)), a, b);
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
+    unpair(add2(pair(a, b), pair(1.f, 1.f)), a, b);
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+    return mul2(x, pair(a, b));
+  }
+  unpair(x, a, b);
+  return pair(silu<IO>(a), silu<IO>(b));
 }
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }

@@ -24,30 +24,35 @@ __device__ __forceinline__ void step_size(float x, float A, float& dt, float& a)
 constexpr int kChannels = 4;
 
 template <typename IO, int W>
-struct Filter {
+struct Filter {  // pairs of channels, for packed FMAs
   using Vc = Vec<IO, kChannels>;
-  static constexpr int V = kChannels;
-  float w[W][V], b[V];
+  using Row = f32x2[kChannels / 2];
+  Row w[W], b;
   __device__ __forceinline__ void load(const InputsParams& p, int c0) {
-    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4 bb = p.bias ? *reinterpret_cast<const float4*>(p.bias + c0) : z;
-    b[0] = bb.x, b[1] = bb.y, b[2] = bb.z, b[3] = bb.w;
+    const ulonglong2 bb = p.bias ? *reinterpret_cast<const ulonglong2*>(p.bias + c0) : make_ulonglong2(0, 0);
+    b[0] = bb.x, b[1] = bb.y;
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-      const float4 ww = *reinterpret_cast<const float4*>(p.w + (size_t)i * p.D + c0);
-      w[i][0] = ww.x, w[i][1] = ww.y, w[i][2] = ww.z, w[i][3] = ww.w;
+      const ulonglong2 ww = *reinterpret_cast<const ulonglong2*>(p.w + (size_t)i * p.D + c0);
+      w[i][0] = ww.x, w[i][1] = ww.y;
     }
   }
+  __device__ __forceinline__ static void unpack(typename Vc::raw u, Row& r) {
+    float f[kChannels];
+    Vc::unpack(u, f);
+    r[0] = pair(f[0], f[1]), r[1] = pair(f[2], f[3]);
+  }
   // the output of `x` after the rows `hist`, which it then joins
-  __device__ __forceinline__ typename Vc::raw step(float (*hist)[V], typename Vc::raw xu) const {
-    float x[V], o[V];
-    Vc::unpack(xu, x);
+  __device__ __forceinline__ typename Vc::raw step(Row* hist, typename Vc::raw xu) const {
+    Row x;
+    unpack(xu, x);
+    float o[kChannels];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      float acc = b[j];
+    for (int j = 0; j < kChannels / 2; ++j) {
+      f32x2 acc = b[j];
 #pragma unroll
-      for (int i = 0; i < W - 1; ++i) acc = fmaf(w[i][j], hist[i][j], acc);
-      o[j] = silu<IO>(fmaf(w[W - 1][j], x[j], acc));
+      for (int i = 0; i < W - 1; ++i) acc = fma2(w[i][j], hist[i][j], acc);
+      unpair(silu2<IO>(fma2(w[W - 1][j], x[j], acc)), o[2 * j], o[2 * j + 1]);
 #pragma unroll
       for (int i = 0; i + 1 < W - 1; ++i) hist[i][j] = hist[i + 1][j];
       hist[W - 2][j] = x[j];
@@ -55,6 +60,14 @@ struct Filter {
     return Vc::pack(o);
   }
 };
+
+// a vector of inputs into shared memory, on its way until its group is waited for
+__device__ __forceinline__ void copy_async(uint2* dst, const uint8_t* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async(uint4* dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
 
 // Where the vector of channels [c0, c0 + V) goes: v, k or q (a vector never straddles two:
 // P and N are multiples of 8).
@@ -78,11 +91,13 @@ __device__ __forceinline__ Dest dest_of(const InputsParams& p, int c0) {
 // width - 2 tokens after it, wherever they lie, and writes the sequence's new state, so
 // that the thread that writes a state element is the only one that reads it.
 template <typename IO, int W>
-__global__ void __launch_bounds__(kThreadsIn, 6) prompt_inputs_kernel(const __grid_constant__ InputsParams p) {
+__global__ void __launch_bounds__(kThreadsIn, sizeof(IO) == 2 ? 6 : 4) prompt_inputs_kernel(const __grid_constant__ InputsParams p) {
   using Vc = Vec<IO, kChannels>;
   using Raw = typename Vc::raw;
   constexpr int V = kChannels, K = W - 1;
-  constexpr int U = 4;  // tokens whose loads are in flight together
+  constexpr int U = 4;  // tokens of a group; the groups of a ring are in flight together
+  constexpr int kRing = 4;
+  __shared__ Raw ring[kRing][U][kThreadsIn];  // each thread's own: no barriers
   pdl_enter();
   const Packed& pk = p.pk;
   // blocks of the same tokens are neighbours, so that the rows are read as a whole
@@ -143,16 +158,19 @@ __global__ void __launch_bounds__(kThreadsIn, 6) prompt_inputs_kernel(const __gr
     if (!on) continue;
     const uint8_t* xt = x + (size_t)ta * xs;
     uint8_t* yt = d.base + (size_t)ta * d.stride;
-    int left = (int)(tb - ta);
-    // two groups of U tokens: one in flight while the other is computed
-    Raw xu[2][U];
-    auto fetch = [&](Raw* g) {  // the next U tokens from xt on, as far as there are any
+    const int count = (int)(tb - ta);
+    int asked = 0;  // tokens whose copies were issued
+    auto fetch = [&](int g) {  // the next U tokens into the ring's group g, as far as there are any
 #pragma unroll
-      for (int u = 0; u < U; ++u) g[u] = u < left ? __ldg(reinterpret_cast<const Raw*>(xt + u * xs)) : Vc::zero();
+      for (int u = 0; u < U; ++u)
+        if (asked + u < count) copy_async(&ring[g][u][threadIdx.x], xt + u * xs);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      asked += U;
       xt += U * xs;
     };
-    fetch(xu[0]);
-    float hist[K][V];
+#pragma unroll
+    for (int g = 0; g < kRing - 1; ++g) fetch(g);
+    typename Filter<IO, W>::Row hist[K];
     if (owner) {
       Raw old[K];
       Raw* st = reinterpret_cast<Raw*>(static_cast<uint8_t*>(p.conv) + ((size_t)row * K * p.D + c0) * sizeof(IO));
@@ -160,7 +178,7 @@ __global__ void __launch_bounds__(kThreadsIn, 6) prompt_inputs_kernel(const __gr
 #pragma unroll
       for (int i = 0; i < K; ++i) {
         old[i] = res ? st[i * ss] : Vc::zero();
-        Vc::unpack(old[i], hist[i]);
+        f.unpack(old[i], hist[i]);
       }
       const int64_t n = end - begin;
 #pragma unroll
@@ -177,24 +195,19 @@ __global__ void __launch_bounds__(kThreadsIn, 6) prompt_inputs_kernel(const __gr
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < K; ++i) Vc::unpack(x_at(ta - K + i), hist[i]);
+      for (int i = 0; i < K; ++i) f.unpack(x_at(ta - K + i), hist[i]);
     }
-    auto put = [&](const Raw* g, int n) {
+    int g = 0;
+    for (int t = 0; t < count; t += U) {
+      fetch(g == 0 ? kRing - 1 : g - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (u < n) *reinterpret_cast<Raw*>(yt + u * d.stride) = f.step(hist, g[u]);
+        if (t + u < count) *reinterpret_cast<Raw*>(yt + u * d.stride) = f.step(hist, ring[g][u][threadIdx.x]);
       yt += U * d.stride;
-    };
-    while (left > 0) {
-      int n = left;
-      left -= U;
-      fetch(xu[1]);
-      put(xu[0], n);
-      n = left;
-      left -= U;
-      fetch(xu[0]);
-      put(xu[1], n);
+      g = g == kRing - 1 ? 0 : g + 1;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
 }
 
@@ -277,11 +290,11 @@ __global__ void __launch_bounds__(kThreadsIn) token_inputs_kernel(const __grid_c
 #pragma unroll
     for (int u = 0; u < R; ++u) {
       if (row[u] < 0) continue;
-      float hist[K][V];
+      typename Filter<IO, W>::Row hist[K];
       Raw* st = reinterpret_cast<Raw*>(static_cast<uint8_t*>(p.conv) + ((size_t)row[u] * K * p.D + c0) * sizeof(IO));
 #pragma unroll
       for (int i = 0; i < K; ++i) {
-        Vc::unpack(old[u][i], hist[i]);
+        f.unpack(old[u][i], hist[i]);
         st[i * ss] = i + 1 < K ? old[u][i + 1 < K ? i + 1 : i] : xu[u];
       }
       const Raw o = f.step(hist, xu[u]);
