@@ -43,20 +43,26 @@ FALLBACK_HBM_GBS = 6650.0
 # DRAM traffic of one replay_step launch (flush and output-only launches averaged over a
 # window) of the workload it was captured on, from an ncu capture, and the hash of the
 # kernel sources it applies to. For another workload, or once the sources change, the
-# figure does not apply and is reported as null. "captured_on" is the hash of the sources
-# of the capture itself (they differ from the current ones only in the kernel's header
-# comment and in two unused device helpers since removed). Measured on the fold launch
+# figure does not apply and is reported as null. The hash covers the decode kernels' sources.
+# "captured_on" is that of every source at the capture itself (the decode kernels' differ
+# from the current ones only in the kernel's header comment and in two unused device helpers
+# since removed). Measured on the fold launch
 # and an 8-entry output-only launch: (fold + 15 x output-only) / 16.
 NCU_TRAFFIC = {"workload": "mamba2_b256",
-               "sources_sha256": "ca5c0a8c8f3c97581a3b95deec93766a80041e023cd01d3a2fcda67ef3bd8f8a",
+               "sources_sha256": "8b1a1e36f94d6b68f313ab777865c1610482210ba78a3f2ab8c64abc701e13ed",
                "captured_on": "e21d8dddf37eccd0f0edeb00f8e98d6b152826fcde7bec1dd8fcedccd8204fe7",
                "bytes_per_launch": 646.1e6}
+
+
+DECODE_SOURCES = ("replay_device.cuh", "replay_instances.cuh", "replay_kernel.cuh", "replay_kernels_n128.cu",
+                  "replay_kernels_n16.cu", "replay_kernels_n32.cu", "replay_kernels_n64.cu", "replay_kparams.h",
+                  "replay_launch.h", "replay_small.cu")
 
 
 def kernel_sources_hash() -> str:
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "linear_attention_decode_replay_b200", "csrc")
-    for f in sorted(os.listdir(csrc)):
+    for f in DECODE_SOURCES:
         with open(os.path.join(csrc, f), "rb") as fh:
             h.update(f.encode())
             h.update(fh.read())
