@@ -2,8 +2,11 @@
 //   c_t = bias + sum_i w[i] x[t - (width - 1) + i]   (within the sequence; before its first
 //                                                    token: the stored rows, or zero)
 //   v | k | q = c_t sigmoid(c_t),   Delta = softplus(raw + dt_bias),   a = exp(-Delta A).
-// One pass: every channel is read once and written once, so both kernels are bound by
-// memory bandwidth. Sums are FP32; q, k and v are rounded once, to the layer's io type.
+// One pass: every channel is read once and written once, so memory bandwidth bounds both
+// kernels; the exponential and the reciprocal of each output take half of what the special
+// function unit can do in that time. Sums are FP32; q, k and v are rounded once, to the
+// layer's io type. 8192 tokens of 20480 BF16 channels: 134 us, 78 % of the measured copy
+// bandwidth; one token of 256 such rows: 18 us, 73 %.
 #include "layer_device.cuh"
 
 namespace replay {
@@ -85,9 +88,10 @@ __device__ __forceinline__ Dest dest_of(const InputsParams& p, int c0) {
 
 }  // namespace
 
-// Packed prompts. A block takes a tile of tokens and kThreadsIn vectors of channels (the
-// last one of a tile: its step sizes); a thread walks its tokens with the filter's
-// rows in registers. The tile that holds a sequence's first token also takes the
+// Packed prompts. A block takes a tile of tokens and kThreadsIn vectors of channels (the last
+// one of a tile: its step sizes); a thread walks its tokens with the filter's rows in
+// registers, and the tokens ahead on their way into shared memory (in registers they cost
+// warps: 143 against 134 us). The tile that holds a sequence's first token also takes the
 // width - 2 tokens after it, wherever they lie, and writes the sequence's new state, so
 // that the thread that writes a state element is the only one that reads it.
 template <typename IO, int W>

@@ -4,13 +4,23 @@
 //   Y1 = P V,  P_ij = C_ij r_ij Delta_j (j <= i)
 //   Y2 = Q S^T                          S   <- abar_Q S + dS
 //   dS = U^T K, U_j = (Delta_j prod_{l > j} a_l) v_j
-// A block walks one head of one sequence (64 of its P rows). q, k and v come by TMA into
-// 128-byte swizzled tiles; C, Y1, Y2 and dS are tensor-memory accumulators; S stays in
-// registers, one state column n a thread. FP32 factors enter the products as sums of BF16
-// parts: U in three (remainder 2^-24: the state keeps FP32 accuracy), S and P in two
-// (remainder 2^-17, under the outputs' own rounding of 2^-9). dS is summed apart from S,
-// since the accumulators do not round to nearest and S may hold thousands of tokens.
-// Decays are products, never exponentials of differences: a = 0 and any sign are exact.
+// A block walks units, a head of a sequence (64 of its P rows) each, longest sequences first.
+// q, k and v come by TMA into 128-byte swizzled tiles; C, Y1, Y2 and dS are accumulators in
+// tensor memory; S stays in registers, half a state column n a thread. FP32 factors enter the
+// products as sums of BF16 parts: U in three (what is left is under 2^-24 of it, so that the
+// state keeps FP32 accuracy), S and P in two (2^-16, under the outputs' own rounding of 2^-8).
+// dS is summed apart from S, since the accumulators do not round to nearest and S may hold
+// thousands of tokens. Decays are products, never exponentials of differences: a = 0 and any
+// sign are exact. A few long sequences are cut into segments: the segments' own states first
+// (LOCAL: k and v only), then the states that they start from, then all segments at once.
+//
+// What bounds it: a chunk of one head at N = 128 takes an SM about 4900 cycles. Its products
+// are 2300 of them, its traffic in shared memory (tiles in and out, operands) about 3700, its
+// instructions 2400 a scheduler; the chain C - P - Y1 within a chunk, whose P lies where the
+// next C will (tensor memory is full), keeps them from overlapping further. 8192 tokens of
+// the 64-head layer (G = 64): 105 us, 62 % of the measured copy bandwidth; 32768 tokens of one
+// sequence (G = 8): 500-550 us, of which 160 us the segments' own states. One part each for P
+// and S gained 7 % and cost the outputs 40 % of their accuracy: left at two.
 #include "layer_device.cuh"
 #include "tcgen05.cuh"
 
@@ -38,8 +48,7 @@ struct alignas(64) ScanTcParams {
 };
 
 // Tensor memory columns. P lies over C: the two BF16 parts of 16 columns of P take the 16
-// columns that held C's.
-// (LOCAL: two of dS alone).
+// columns that held C's. (LOCAL: two buffers of dS alone.)
 constexpr uint32_t kColC = 0, kColY1 = 128, kColY2 = 192, kColDS = 320;
 
 // A block's next unit: tokens [begin, begin + len) of one sequence, 64 state rows from p0 of
@@ -432,8 +441,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
         if (!(ok = wait2_warp(&bars->da_full[n % kSlots], n / kSlots, &bars->c_full, n))) break;
         tc_fence_after();
         const float pre = d.pre[i];
-        // Half 0 takes the diagonal block of 32 columns, half 1 those before it. The loops stay small: four warps with code of their own
-        // share an instruction cache, and unrolled they waited for instructions.
+        // Half 0 takes the diagonal block of 32 columns, half 1 those before it. The loops stay
+        // small: the roles share an instruction cache, and unrolled they waited for instructions.
         if (half == 0) {
           const float4* da = reinterpret_cast<const float4*>(d.da + 32 * w4);
           float rd = 0.f;
