@@ -15,12 +15,12 @@
 // (LOCAL: k and v only), then the states that they start from, then all segments at once.
 //
 // What bounds it: a chunk of one head at N = 128 takes an SM about 4900 cycles. Its products
-// are 2300 of them, its traffic in shared memory (tiles in and out, operands) about 3700, its
-// instructions 2400 a scheduler; the chain C - P - Y1 within a chunk, whose P lies where the
+// are 2300 of them (tensor pipe 46 % active), its wavefronts in the shared-memory pipe 2900, its
+// instructions 2600 a scheduler; the chain C - P - Y1 within a chunk, whose P lies where the
 // next C will (tensor memory is full), keeps them from overlapping further. 8192 tokens of
-// the 64-head layer (G = 64): 105 us, 62 % of the measured copy bandwidth; 32768 tokens of one
-// sequence (G = 8): 500-550 us, of which 160 us the segments' own states. One part each for P
-// and S gained 7 % and cost the outputs 40 % of their accuracy: left at two.
+// the 64-head layer (G = 64): 107 us, 61 % of the measured copy bandwidth; 32768 tokens of one
+// sequence (G = 8): 530 us, of which 165 us the segments' own states. One part each for P
+// and S gained 3 to 5 % and raised the outputs' error from 1.7e-3 to 2.3e-3: left at two.
 #include "layer_device.cuh"
 #include "tcgen05.cuh"
 
