@@ -93,10 +93,11 @@ int check_scratch(const void* scratch, int64_t have, int64_t need) {
 // The serial kernel takes FP32 inputs, and BF16 sequences of few tokens, where the tensor
 // cores' chunks of 128 are mostly empty: a chunk of one head takes an SM about 6 us with its
 // state, a token of the serial kernel 0.27 us in each of a few blocks an SM (256 sequences of
-// the 64-head layer: 16 tokens each 443 against 672 us, 32 tokens 743 against 670 us).
+// the 64-head layer: 16 tokens each 380 against 672 us, 24 tokens 526 against 668 us, 32 tokens 689 against
+// 673 us).
 bool on_tensor_cores(const replay_config& c, int64_t tokens, int32_t n_seqs, int64_t max_len) {
   if (c.io != REPLAY_BF16 || tokens == 0) return false;
-  constexpr int64_t kFew = 24;
+  constexpr int64_t kFew = 30;
   if (tokens > kFew * n_seqs) return true;
   const int64_t longest = max_len > 0 && max_len < tokens ? max_len : tokens;
   const int64_t units = (int64_t)n_seqs * c.heads * ((c.P + 63) / 64);

@@ -3,9 +3,11 @@
 // A block holds a block of state rows of one head of one sequence in registers and walks
 // the sequence's tokens; a thread holds kRows rows of kCols columns. All arithmetic is
 // FP32, as packed pairs (three instructions for two elements a token). It serves every size
-// and type. The shared-memory pipe bounds it where there are enough blocks (four prompts of
-// 2050 FP32 tokens in all, 64 heads of 64 x 128: 228 us, that pipe 84 % busy handing k and q
-// to the threads, the FMA pipe 52 %), a token's chain where there are few.
+// and type. Handing k and q to the threads loads the shared-memory pipe about as much as the
+// FMAs load theirs: four rows of 8 columns a thread read half of what two of 16 do. Four
+// prompts of 2050 FP32 tokens in all, 64 heads of 64 x 128: 206 us (two rows: 223 us, that pipe
+// 84 % busy; now 63 %, the FMA pipe 59 %). What is left there is few warps (11 % of an SM's)
+// and blocks of unequal length; where there are few blocks, a token's chain.
 #include "layer_device.cuh"
 #include "tcgen05.cuh"
 
@@ -14,12 +16,12 @@ namespace replay {
 namespace {
 
 constexpr int kSerialThreads = 128;
-constexpr int kRows = 2, kCols = 16;
+constexpr int kRows = 4, kCols = 8;
 
 // Tokens staged in shared memory together, and tokens whose sums over a row's lanes are taken
 // together: short BF16 sequences want little staging and many blocks an SM (256 sequences of
-// one token: 209 us with 8 and 4, 305 us with 16 and 8), FP32 prompts few barriers and sums
-// (four of 500 tokens: 219 us with 16 and 8, 270 us with 8 and 4).
+// one token: 194 us; with two rows a thread 209 us, and 305 us with 16 and 8), FP32 prompts few
+// barriers and sums (four of 2050 in all: 206 us with 16 and 8, 218 us with 16 and 4).
 template <typename IO, int N>
 constexpr int serial_tokens() {
   return sizeof(IO) == 2 || N == 16 ? 8 : 16;
@@ -133,10 +135,11 @@ __global__ void __launch_bounds__(kSerialThreads, sizeof(IO) == 2 ? 4 : 1) scan_
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         const float2 da = sda[b][tb + u];
-        const float2 vv = *reinterpret_cast<const float2*>(&sv[b][tb + u][r0]);
+        const float4 vv = *reinterpret_cast<const float4*>(&sv[b][tb + u][r0]);
         const f32x2 a2 = pair(da.y, da.y);
-        const f32x2 w2[kRows] = {pair(da.x * vv.x, da.x * vv.x), pair(da.x * vv.y, da.x * vv.y)};
-        f32x2 y2[kRows] = {0, 0};
+        const f32x2 w2[kRows] = {pair(da.x * vv.x, da.x * vv.x), pair(da.x * vv.y, da.x * vv.y),
+                                 pair(da.x * vv.z, da.x * vv.z), pair(da.x * vv.w, da.x * vv.w)};
+        f32x2 y2[kRows] = {};
 #pragma unroll
         for (int i = 0; i < kCols / 4; ++i) {
           const ulonglong2 kk = *reinterpret_cast<const ulonglong2*>(&sk[b][tb + u][4 * (lane + TPR * i)]);
