@@ -428,6 +428,8 @@ class Replay:
         """prompt_scan() into the layer: packed prompts become the states that step() decodes
         on from. Sequence i is the layer's sequence seqs[i]; where resume[i], it continues
         from that sequence's checkpoint and buffered entries. Returns y [T][H][P] io."""
+        if not isinstance(q, torch.Tensor):
+            raise TypeError("q must be a torch.Tensor")
         dev, T = self.buffers["S0"].get_device(), q.shape[0]
         n, cu, sp, rp = _packed_args(cu_seqlens, seqs, resume, dev)
         ptrs, y_shape = _scan_args(self.cfg, T, q, k, v, dt, a, dev)
@@ -635,6 +637,8 @@ def gated_norm(cfg: Config, y, z, weight, v=None, D=None, norm_groups=1, eps=1e-
     [T][H][P] (FP32 or io), z [T][H*P] (io; rows may be slices of wider ones), weight
     [H*P] FP32; v [T][H][P] (io) and D [H] (FP32) for the skip term. Returns [T][H*P] io."""
     c, t, _, _, vs, hs = cfg._layer
+    if not isinstance(y, torch.Tensor):
+        raise TypeError("y must be a torch.Tensor")
     if y.dtype is not torch.float32 and y.dtype is not t:
         raise ValueError(f"y must have dtype {torch.float32} or {t}, got {y.dtype}")
     dev, T = _device_of(z, "z"), y.shape[0]

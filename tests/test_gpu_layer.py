@@ -272,3 +272,33 @@ def test_a_layer_from_prompt_to_decode(ckpt, io):
     prompt((20, 0, 33), [2, 1, 3], [1, 1, 0], 2)
     decode(6, 300)
     assert layer.check_status() == 0
+
+
+def test_a_prefill_in_a_graph():
+    """A prompt into a layer and two steps, captured: every replay gives what the calls give."""
+    H, G, P, N, B = 4, 2, 24, 32, 2
+    cfg = lar.Config(batch=B, heads=H, groups=G, P=P, N=N, L=3)
+    case = Case("g", H, G, P, N, (140, 70), "bf16", rows=B)
+    r = layer_rows(case)
+    cu = packed(case)[0]
+    ins = lar.prompt_inputs(cfg, r["conv"].clone(), r["x"], r["raw"], r["w"], r["A"], cu)
+    token = [t[:B].contiguous() for t in ins]
+
+    def calls(layer):
+        return [layer.prefill(*ins, cu), layer.step(*token), layer.step(*token)]
+
+    first = lar.Replay(cfg, lar.alloc_buffers(cfg, "cuda"))
+    want = [t.clone() for t in calls(first)]
+    layer = lar.Replay(cfg, lar.alloc_buffers(cfg, "cuda"))
+    calls(layer)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = calls(layer)
+    for _ in range(3):
+        for t in got:
+            t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(want, got))
+        assert torch.equal(layer.buffers["S0"], first.buffers["S0"])
+    assert layer.read_counts() == first.read_counts() and layer.check_status() == 0

@@ -254,3 +254,21 @@ def test_scan_on_another_stream_and_in_a_graph():
     torch.cuda.synchronize()
     want, mag = oracle(ins, cu, None, resume)
     check(other, ins, outs[0], Sg[0], want, mag, cu, None, resume)
+
+
+@pytest.mark.parametrize("P", [8, 40])
+@pytest.mark.parametrize("length", [1, 29, 30, 31, 32])
+def test_lengths_on_both_sides_of_the_choice_of_kernel(length, P):
+    """Short BF16 sequences go token by token, longer ones in chunks: the same bounds for both."""
+    case = Case("choice", 4, 2, P, 128, (length,) * 3, "bf16", resume="some", seed=length)
+    ins = scan_inputs(case)
+    y, S, cu, seqs, resume = run(case, ins)
+    check(case, ins, y, S, *oracle(ins, cu, seqs, resume), cu, seqs, resume)
+
+
+@pytest.mark.parametrize("max_len", [1, 128, 10 ** 9])
+def test_a_wrong_longest_length_only_steers(max_len):
+    case = Case("estimate", 2, 1, 64, 128, (1500, 3), "bf16", resume="all")
+    ins = scan_inputs(case)
+    y, S, cu, seqs, resume = run(case, ins, max_len=max_len)
+    check(case, ins, y, S, *oracle(ins, cu, seqs, resume), cu, seqs, resume)

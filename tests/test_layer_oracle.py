@@ -197,3 +197,14 @@ def test_the_binding_refuses_other_tensors():
         lar.token_inputs(cfg, conv, x, f(3, 4), f(4), f(4))
     with pytest.raises(ValueError, match="cu_seqlens"):
         lar.prompt_scan(cfg, f(2, 4, 16, 16), f(3, 2, 16), f(3, 2, 16), f(3, 4, 16), f(3, 4), f(3, 4), cu[:0])
+
+
+def test_the_binding_refuses_what_is_no_tensor():
+    cfg = lar.Config(batch=2, heads=4, groups=2, P=16, N=16, L=1)
+    f, cu = torch.zeros, torch.tensor([0, 3], dtype=torch.int32)
+    layer = object.__new__(lar.Replay)  # no context: the argument is refused before one is used
+    layer.cfg, layer.buffers, layer._ctx = cfg, {"S0": f(2, 4, 16, 16)}, None
+    with pytest.raises(TypeError, match="y must be"):
+        lar.gated_norm(cfg, [1.0], f(3, 64).bfloat16(), f(64))
+    with pytest.raises(TypeError, match="q must be"):
+        layer.prefill([1.0], f(3, 2, 16), f(3, 4, 16), f(3, 4), f(3, 4), cu)
