@@ -18,7 +18,7 @@
 // are 2300 of them (tensor pipe 46 % active), its wavefronts in the shared-memory pipe 2900, its
 // instructions 2600 a scheduler; the chain C - P - Y1 within a chunk, whose P lies where the
 // next C will (tensor memory is full), keeps them from overlapping further. 8192 tokens of
-// the 64-head layer (G = 64): 107 us, 61 % of the measured copy bandwidth; 32768 tokens of one
+// the 64-head layer (G = 64): 104 us, 63 % of the measured copy bandwidth; 32768 tokens of one
 // sequence (G = 8): 530 us, of which 165 us the segments' own states. One part each for P
 // and S gained 3 to 5 % and raised the outputs' error from 1.7e-3 to 2.3e-3: left at two.
 #include "layer_device.cuh"
