@@ -124,6 +124,13 @@ __global__ void __launch_bounds__(kThreadsIn, sizeof(IO) == 2 ? 6 : 4) prompt_in
   const size_t xs = (size_t)p.ldx * sizeof(IO);
   auto x_at = [&](int64_t t) { return __ldg(reinterpret_cast<const Raw*>(x + (size_t)t * xs)); };
 
+  // Bounds that fall mislead the search below, so that a sequence may be passed over: one block
+  // looks for them, so that they are always reported.
+  if (tile == 0 && steps) {
+    bool falls = false;
+    for (int i = threadIdx.x; i < pk.n_seqs; i += kThreadsIn) falls |= pk.cu[i] > pk.cu[i + 1];
+    if (falls && pk.status) atomicOr(pk.status, kErrSeqs);
+  }
   // the first sequence that starts in this tile or after it: 32 bounds at a time
   int lo = 0, hi = pk.n_seqs;
   while (lo < hi) {
@@ -138,11 +145,11 @@ __global__ void __launch_bounds__(kThreadsIn, sizeof(IO) == 2 ? 6 : 4) prompt_in
     lo += (n - 1) * hop + 1;
   }
   for (int s = lo > 0 ? lo - 1 : 0; s < pk.n_seqs; ++s) {
-    const bool owner = s >= lo;
-    if (owner && !(pk.cu[s] < t1 || last)) break;
+    if (s >= lo && !(pk.cu[s] < t1 || last)) break;
     int64_t begin, end;
-    const bool res = owner && pk.resume && pk.resume[s];  // on its way with the bounds and the row
+    const bool res = s >= lo && pk.resume && pk.resume[s];  // on its way with the bounds and the row
     if (!seq_bounds(pk, s, begin, end)) continue;
+    const bool owner = s >= lo && begin >= t0;  // it starts in this tile, and so in no other's, whatever the order
     const int64_t ta = owner ? begin : (t0 > begin + K ? t0 : begin + K);
     const int64_t to = !owner || t1 > begin + K ? t1 : begin + K;
     const int64_t tb = end < to ? end : to;

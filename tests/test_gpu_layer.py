@@ -302,3 +302,69 @@ def test_a_prefill_in_a_graph():
         assert all(torch.equal(x, y) for x, y in zip(want, got))
         assert torch.equal(layer.buffers["S0"], first.buffers["S0"])
     assert layer.read_counts() == first.read_counts() and layer.check_status() == 0
+
+
+def good_sequences(bounds, T):
+    """The sequences whose own bounds are good, and how many of them hold each token."""
+    good = [s for s in range(len(bounds) - 1) if 0 <= bounds[s] <= bounds[s + 1] <= T]
+    held = np.zeros(T, int)
+    for s in good:
+        held[bounds[s]:bounds[s + 1]] += 1
+    return good, held
+
+
+BAD_BOUNDS = {
+    "falls": (60, [0, 10, 5, 60]),
+    "falls_far": (100, [0, 100, 40, 60]),
+    "falls_outside": (60, [0, 10, 500, 30, 60]),
+    "all_down": (60, [60, 40, 20, 0]),
+    # the mistake behind what one look of the search sees
+    "falls_late": (900, [3 * i for i in range(280)] + [100, 850, 900]),
+    "before": (60, [-4, 10, 30, 60]),
+    "all_before": (60, [-9, -4, 0, 60]),
+    "past": (60, [0, 10, 30, 61]),
+    "far_past": (60, [0, 10, 10, 2 ** 31 - 1, 2 ** 31 - 1]),
+}
+
+
+@pytest.mark.parametrize("resume", ["none", "all"])
+@pytest.mark.parametrize("name", BAD_BOUNDS)
+def test_inputs_with_bad_bounds(name, resume):
+    """Sequences with bad bounds are skipped and reported. Where no bounds fall the others have
+    their outputs and states; where some do, every state is the old one or the right one, and
+    every token that one sequence alone holds has its outputs or those it had."""
+    T, bounds = BAD_BOUNDS[name]
+    n = len(bounds) - 1
+    falls = any(b < a for a, b in zip(bounds, bounds[1:]))
+    case = Case(name, 3, 1, 24, 32, (T,), "bf16", rows=n + 2)
+    r = layer_rows(case)
+    cu = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    seqs = torch.arange(n, 0, -1, dtype=torch.int32, device="cuda")
+    on = torch.ones(n, dtype=torch.uint8, device="cuda") if resume == "all" else None
+    conv, status = r["conv"].clone(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    q, k, v, dt, a = out = tuple(torch.full(s, 7.0, device="cuda", dtype=d) for s, d in
+                                 (((T, 1, 32), case.dtype), ((T, 1, 32), case.dtype), ((T, 3, 24), case.dtype),
+                                  ((T, 3), torch.float32), ((T, 3), torch.float32)))
+    lar.prompt_inputs(case.cfg(), conv, r["x"], r["raw"], r["w"], r["A"], cu, seqs=seqs, resume=on, out=out,
+                      status=status)
+    assert status.item() == _abi.DEV_SEQS
+    good, held = good_sequences(bounds, T)
+    old, new = f64(r["conv"]), f64(conv)
+    same = lambda x: f64((x == 7).flatten(1).all(1)).astype(bool)  # noqa: E731
+    untouched = [same(x) for x in out]
+    for x in untouched:
+        assert x[held == 0].all()
+    if not falls:
+        assert not any(x[held > 0].any() for x in untouched)
+    written = ~np.any(untouched[:3], axis=0)  # some columns' block may pass over a token that another's serves
+    for s in range(n):
+        row = n - s
+        if s not in good:
+            assert np.array_equal(new[row], old[row])
+            continue
+        want = lo.prompt_inputs(f64(r["x"]), f64(r["raw"]), f64(r["w"]), None, None, f64(r["A"]), old,
+                                bounds[s:s + 2], [row], None if on is None else [1])
+        check_inputs(case, (q, k, v, dt, a, conv), want, np.isfinite(want[1][:, 0]) & (held == 1) & written)
+        right = np.array_equal(new[row], want[3][row])
+        assert right or (falls and np.array_equal(new[row], old[row]))
+    assert np.array_equal(new[[0, n + 1]], old[[0, n + 1]])
