@@ -64,6 +64,7 @@ struct TcBars {
   uint64_t c_full, p_full, y_full, y_free, u_full[2], ds_full[2], ds_free[2], s_full, da_full[kSlots], drain[2];
   uint64_t unit_full[2], unit_empty[2];
   uint32_t tmem, abort;
+  int seg_tokens;  // of a segment, or more than any sequence has
   Unit unit[2];
   int order[kSortSeqs];
 };
@@ -116,17 +117,30 @@ __device__ __forceinline__ void store_sector(void* dst, const uint32_t* r) {
 
 }  // namespace
 
+// The segments of sequence s (one, where its bounds are bad).
+__device__ __forceinline__ int segments_of(const Packed& pk, int seg_tokens, int s) {
+  const int64_t len = (int64_t)pk.cu[s + 1] - pk.cu[s];
+  return len > seg_tokens && len <= pk.tokens ? (int)((len + seg_tokens - 1) / seg_tokens) : 1;
+}
+
+// Whether all segments have their place, by a whole warp. Sequences that share tokens, where
+// bounds fall, can have more than the tokens allow; then every sequence is taken whole.
+__device__ __forceinline__ bool segments_fit(const Packed& pk, int seg_tokens, int max_segs) {
+  int n = 0;
+#pragma unroll 1
+  for (int s = threadIdx.x & 31; s < pk.n_seqs; s += 32) n = min(n + segments_of(pk, seg_tokens, s), 1 << 25);
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
+  return n <= max_segs;
+}
+
 // Segment number `seg` of the packed sequences' segments: its sequence, its place among the
 // sequence's, and how many those are. Whole warps; false past the last segment.
 __device__ __forceinline__ bool find_segment(const Packed& pk, int seg_tokens, int seg, int& s, int& m, int& of) {
   const int lane = threadIdx.x & 31;
   int before = 0;
   for (int s0 = 0; s0 < pk.n_seqs; s0 += 32) {
-    int n = 0;
-    if (s0 + lane < pk.n_seqs) {
-      const int64_t len = (int64_t)pk.cu[s0 + lane + 1] - pk.cu[s0 + lane];
-      n = len > seg_tokens && len <= pk.tokens ? (int)((len + seg_tokens - 1) / seg_tokens) : 1;
-    }
+    const int n = s0 + lane < pk.n_seqs ? segments_of(pk, seg_tokens, s0 + lane) : 0;
     int upto = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -181,11 +195,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   if (warp == kWarpTma) tmem_alloc(&bars->tmem, 512);
+  if (warp == kWarpPlan) {
+    const bool fit = !p.seg_tokens || segments_fit(p.pk, p.seg_tokens, p.max_segs);
+    if (lane == 0) bars->seg_tokens = fit ? p.seg_tokens : INT32_MAX;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(bars->tmem);
   volatile uint32_t* abort = &bars->abort;
+  volatile int* seg_tokens = &bars->seg_tokens;
 
   // waits for a phase; false if it takes too long (the block then winds down: every other
   // wait of its ends within the same time)
@@ -259,7 +278,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
         if (more) {
           if (id >= tp.units) continue;
           int s = id / heads, seg = 0, segs = 1;
-          if (p.seg_tokens && !find_segment(p.pk, p.seg_tokens, s, s, seg, segs)) continue;
+          if (p.seg_tokens && !find_segment(p.pk, *seg_tokens, s, s, seg, segs)) continue;
           if (LOCAL && seg == segs - 1) continue;
           if (sorted) s = bars->order[s];
           int64_t begin, end;
@@ -772,15 +791,12 @@ __global__ void __launch_bounds__(256) scan_carry_kernel(const __grid_constant__
   if (segs <= 1) return;
   const int row = seq_row(p.pk, s);
   if (row < 0) return;
+  if (!segments_fit(p.pk, p.seg_tokens, p.max_segs)) return;
   // segments before this sequence's
   int first = 0;
-  for (int e = threadIdx.x & 31; e < s; e += 32) {
-    const int64_t len = (int64_t)p.pk.cu[e + 1] - p.pk.cu[e];
-    first += len > p.seg_tokens && len <= p.pk.tokens ? (int)((len + p.seg_tokens - 1) / p.seg_tokens) : 1;
-  }
+  for (int e = threadIdx.x & 31; e < s; e += 32) first += segments_of(p.pk, p.seg_tokens, e);
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) first += __shfl_xor_sync(0xffffffffu, first, off);
-  if (first + segs > p.max_segs) return;  // only where bounds are out of order
   const int ptiles = (p.P + kPT - 1) / kPT;
   const bool res = p.pk.resume && p.pk.resume[s];
   const int vecs = p.P * p.N / 4;

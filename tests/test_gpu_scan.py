@@ -272,3 +272,32 @@ def test_a_wrong_longest_length_only_steers(max_len):
     ins = scan_inputs(case)
     y, S, cu, seqs, resume = run(case, ins, max_len=max_len)
     check(case, ins, y, S, *oracle(ins, cu, seqs, resume), cu, seqs, resume)
+
+
+@pytest.mark.parametrize("resume", ["none", "all"])
+@pytest.mark.parametrize("bounds", [[0, 5000, 100, 4900, 5000], [0, 2500, 0, 5000, 7000, 5000], [5000, 0, 5000, 0, 5000]])
+def test_long_sequences_beside_bad_bounds(bounds, resume):
+    """Long sequences are cut into segments, and sequences that share tokens have more of them
+    than the tokens allow: each sequence with good bounds still ends in its own state."""
+    n = len(bounds) - 1
+    case = Case("fall", 2, 1, 64, 128, (5000,), "bf16", rows=n)
+    q, k, v, dt, a, S = ins = scan_inputs(case)
+    cu = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    on = torch.ones(n, dtype=torch.uint8, device="cuda") if resume == "all" else None
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    S1 = S.clone()
+    y = lar.prompt_scan(case.cfg(), S1, q, k, v, dt, a, cu, resume=on, status=status)
+    assert status.item() == _abi.DEV_SEQS
+    good = [s for s in range(n) if 0 <= bounds[s] <= bounds[s + 1] <= case.T]
+    held = sum(((np.arange(case.T) >= bounds[s]) & (np.arange(case.T) < bounds[s + 1])).astype(int) for s in good)
+    for s in range(n):
+        if s not in good:
+            assert torch.equal(S1[s], S[s])
+            continue
+        args = [f64(t) for t in ins] + [bounds[s:s + 2], [s], None if on is None else [1]]
+        (wy, wS), (my, mS) = lo.prompt_scan(*args), lo.prompt_scan_magnitude(*args)
+        roundings = (2 * (bounds[s + 1] - bounds[s]) + case.N + 8) * U32
+        assert_within(S1[s], wS[s], roundings * mS[s] + 1e-37, f"S of {s}")
+        alone = np.isfinite(wy[:, 0, 0]) & (held == 1)
+        by = (roundings + 2.0 ** -14) * my + HALF["bf16"] * np.abs(wy) + 1e-37
+        assert_within(f64(y)[alone], wy[alone], by[alone], f"y of {s}")
