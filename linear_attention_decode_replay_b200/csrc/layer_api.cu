@@ -258,8 +258,8 @@ int replay_gated_norm(const replay_config* cfg, int64_t rows, const void* y, int
     return REPLAY_EINVAL;
   if (width / 8 * (cfg->P / 8) >= INT32_MAX || rows > INT32_MAX / norm_groups) return REPLAY_EINVAL;
   if (y_type != REPLAY_F32 && y_type != cfg->io) return REPLAY_EINVAL;
-  if (!weight || (!v) != (!D) || ldz < width || !(eps >= 0.f)) return REPLAY_EINVAL;
-  if (rows > 0 && (!y || !z || !out)) return REPLAY_EINVAL;
+  if (!weight || ldz < width || !(eps >= 0.f)) return REPLAY_EINVAL;
+  if (rows > 0 && (!y || !z || !out || (!v) != (!D))) return REPLAY_EINVAL;  // no rows: their pointers may be null
   if (!aligned(y, 16) || !aligned(z, 16) || (ldz * io_bytes(*cfg)) % 16 || !aligned(v, 16) || !aligned(out, 16) ||
       !aligned(D, 4) || !aligned(weight, 16))
     return REPLAY_EALIGN;

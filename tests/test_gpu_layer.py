@@ -368,3 +368,22 @@ def test_inputs_with_bad_bounds(name, resume):
         right = np.array_equal(new[row], want[3][row])
         assert right or (falls and np.array_equal(new[row], old[row]))
     assert np.array_equal(new[[0, n + 1]], old[[0, n + 1]])
+
+
+def test_the_whole_path_without_tokens():
+    """A step of a serving loop that has no prompt: every call takes it, and nothing changes."""
+    case = Case("empty", 4, 2, 24, 32, (0,), "bf16", rows=3)
+    cfg = case.cfg()
+    layer = lar.Replay(cfg, lar.alloc_buffers(cfg, "cuda"))
+    layer.buffers["S0"].normal_()
+    r = layer_rows(case)
+    S0, conv = layer.buffers["S0"].clone(), r["conv"].clone()
+    cu, seqs, _ = packed(case)
+    for n in (1, 0):  # a sequence without tokens (it keeps its state), and no sequence
+        on = torch.ones(n, dtype=torch.uint8, device="cuda")
+        q, k, v, dt, a = lar.prompt_inputs(cfg, conv, r["x"], r["raw"], r["w"], r["A"], cu[:n + 1], seqs=seqs[:n], resume=on)
+        y = layer.prefill(q, k, v, dt, a, cu[:n + 1], seqs=seqs[:n], resume=on)
+        o = lar.gated_norm(cfg, y, r["z"], torch.ones(case.H * case.P, device="cuda"), v=v,
+                           D=torch.ones(case.H, device="cuda"))
+        assert o.shape == (0, case.H * case.P) and o.dtype == case.dtype
+    assert torch.equal(layer.buffers["S0"], S0) and torch.equal(conv, r["conv"]) and layer.check_status() == 0

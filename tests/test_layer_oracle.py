@@ -208,3 +208,9 @@ def test_the_binding_refuses_what_is_no_tensor():
         lar.gated_norm(cfg, [1.0], f(3, 64).bfloat16(), f(64))
     with pytest.raises(TypeError, match="q must be"):
         layer.prefill([1.0], f(3, 2, 16), f(3, 4, 16), f(3, 4), f(3, 4), cu)
+
+
+def test_a_norm_of_no_rows_with_the_skip_term():
+    """Without rows v, like y, z and out, has no address; D has its own."""
+    assert _norm(rows=0, y=None, z=None, out=None, v=None, D=P0) == _abi.REPLAY_OK
+    assert _norm(rows=1, v=None, D=P0) == _abi.REPLAY_EINVAL
