@@ -41,7 +41,6 @@ half of the pointer words is current, so capture two windows when L is odd:
 from __future__ import annotations
 
 import ctypes
-import functools
 from dataclasses import dataclass
 
 import torch
@@ -68,8 +67,12 @@ _CKPT = {"f32": _abi.REPLAY_CKPT_F32, "f32_fp8read": _abi.REPLAY_CKPT_F32_FP8REA
          "f32_fp4read": _abi.REPLAY_CKPT_F32_FP4READ}
 
 
+class _Kept:
+    __slots__ = ("_kept",)  # what a Config works out once: in a slot, it is no part of vars() or of pickles
+
+
 @dataclass(frozen=True)
-class Config:
+class Config(_Kept):
     """Sizes of one decode layer (see replay_config in include/replay.h)."""
 
     batch: int
@@ -91,12 +94,20 @@ class Config:
     def io_dtype(self) -> torch.dtype:
         return torch.bfloat16 if self.io == "bf16" else torch.float32
 
-    @functools.cached_property
+    def __getstate__(self):
+        return dict(vars(self))  # the fields: pickled and copied as before any use
+
+    @property
     def _layer(self):
         """What the calls around the step need of it: the C config by reference, the io
         dtype, the channels and the shapes of one token's q (k), v and dt (a)."""
-        H, G, P, N = self.heads, self.groups, self.P, self.N
-        return ctypes.byref(self.c()), self.io_dtype, H * P + 2 * G * N, (G, N), (H, P), (H,)
+        try:
+            return self._kept
+        except AttributeError:
+            H, G, P, N = self.heads, self.groups, self.P, self.N
+            kept = ctypes.byref(self.c()), self.io_dtype, H * P + 2 * G * N, (G, N), (H, P), (H,)
+            object.__setattr__(self, "_kept", kept)
+            return kept
 
 
 def ring_capacity(cfg: Config) -> int:

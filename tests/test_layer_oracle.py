@@ -1,7 +1,10 @@
 """CPU checks of the operators around the decode step: the float64 oracle against torch and
 the decode oracle, and the argument checks of the C ABI (no compute calls)."""
 
+import copy
 import ctypes
+import dataclasses
+import pickle
 
 import numpy as np
 import pytest
@@ -214,3 +217,17 @@ def test_a_norm_of_no_rows_with_the_skip_term():
     """Without rows v, like y, z and out, has no address; D has its own."""
     assert _norm(rows=0, y=None, z=None, out=None, v=None, D=P0) == _abi.REPLAY_OK
     assert _norm(rows=1, v=None, D=P0) == _abi.REPLAY_EINVAL
+
+
+@pytest.mark.parametrize("again", [lambda c: pickle.loads(pickle.dumps(c)), copy.copy, copy.deepcopy,
+                                   lambda c: lar.Config(**vars(c)), lambda c: dataclasses.replace(c)],
+                         ids=["pickle", "copy", "deepcopy", "vars", "replace"])
+def test_a_config_that_was_used_is_copied_like_a_new_one(again):
+    cfg = lar.Config(batch=2, heads=4, groups=2, P=16, N=16, L=1)
+    fields = dict(vars(cfg))
+    with pytest.raises(ValueError, match="CUDA"):
+        lar.gated_norm(cfg, torch.zeros(3, 4, 16), torch.zeros(3, 64).bfloat16(), torch.zeros(64))
+    other = again(cfg)
+    assert other == cfg and hash(other) == hash(cfg) and vars(cfg) == fields == vars(other)
+    with pytest.raises(ValueError, match="CUDA"):
+        lar.gated_norm(other, torch.zeros(3, 4, 16), torch.zeros(3, 64).bfloat16(), torch.zeros(64))
