@@ -21,19 +21,20 @@ struct RefreshParams {
 
 }  // namespace
 
+// Only the rows that the scan then serves: a sequence with bad bounds is skipped, its row's
+// buffered entries stay where they are. (The scan reports it.)
 __global__ void resume_mask_kernel(const __grid_constant__ MaskParams p) {
   pdl_enter();
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
   if (b >= p.pk.batch) return;
+  int s = b;
+  if (p.pk.seqs)
+    for (s = 0; s < p.pk.n_seqs; ++s)
+      if (p.pk.seqs[s] == b) break;  // the first of equal ids is served
   bool on = false;
-  if (p.pk.seqs) {
-    for (int s = 0; s < p.pk.n_seqs; ++s)
-      if (p.pk.seqs[s] == b) {  // the first of equal ids is served
-        on = p.pk.resume[s];
-        break;
-      }
-  } else {
-    on = b < p.pk.n_seqs && p.pk.resume[b];
+  if (s < p.pk.n_seqs) {
+    const int begin = p.pk.cu[s], end = p.pk.cu[s + 1];
+    on = p.pk.resume[s] && begin >= 0 && end >= begin && end <= p.pk.tokens;
   }
   p.mask[b] = on;
 }

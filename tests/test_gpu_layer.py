@@ -387,3 +387,34 @@ def test_the_whole_path_without_tokens():
                            D=torch.ones(case.H, device="cuda"))
         assert o.shape == (0, case.H * case.P) and o.dtype == case.dtype
     assert torch.equal(layer.buffers["S0"], S0) and torch.equal(conv, r["conv"]) and layer.check_status() == 0
+
+
+@pytest.mark.parametrize("bounds", [[0, 10, 30, 61], [0, 10, 60, 30], [-1, 10, 30, 60]])
+@pytest.mark.parametrize("ids", [True, False])
+def test_a_prefill_that_skips_a_sequence_leaves_its_row(bounds, ids):
+    """A continued sequence with bad bounds: its row's checkpoint, count and buffered entries
+    stay, and decode goes on from them; the others' entries are folded."""
+    case = Case("skip", 4, 2, 24, 32, (60,), "bf16", rows=3)
+    cfg = lar.Config(batch=3, heads=4, groups=2, P=24, N=32, L=5)
+    r = layer_rows(case)
+    on = torch.ones(3, dtype=torch.uint8, device="cuda")
+    bad = next(s for s in range(3) if not 0 <= bounds[s] <= bounds[s + 1] <= 60)
+    rows = [2, 0, 1] if ids else [0, 1, 2]
+    cu = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    seqs = torch.tensor(rows, dtype=torch.int32, device="cuda") if ids else None
+    whole = torch.tensor([0, 60], dtype=torch.int32, device="cuda")
+    q, k, v, dt, a = lar.prompt_inputs(cfg, r["conv"].clone(), r["x"], r["raw"], r["w"], r["A"], whole)
+    token = [t[:3].contiguous() for t in (q, k, v, dt, a)]
+    layers = []
+    for _ in range(2):
+        layer = lar.Replay(cfg, lar.alloc_buffers(cfg, "cuda"))
+        layer.buffers["S0"].copy_(torch.linspace(-1, 1, layer.buffers["S0"].numel(), device="cuda").view_as(layer.buffers["S0"]))
+        layer.step(*token)
+        layer.step(*token)
+        layers.append(layer)
+    first, plain = layers
+    first.prefill(q, k, v, dt, a, cu, seqs=seqs, resume=on)
+    row = rows[bad]
+    assert first.read_counts() == [2 if b == row else 0 for b in range(3)]
+    assert torch.equal(first.buffers["S0"][row], plain.buffers["S0"][row])
+    assert torch.equal(first.step(*token)[row], plain.step(*token)[row])
