@@ -301,3 +301,38 @@ def test_long_sequences_beside_bad_bounds(bounds, resume):
         alone = np.isfinite(wy[:, 0, 0]) & (held == 1)
         by = (roundings + 2.0 ** -14) * my + HALF["bf16"] * np.abs(wy) + 1e-37
         assert_within(f64(y)[alone], wy[alone], by[alone], f"y of {s}")
+
+
+def token_by_token(case, ins, S):
+    """Whether a BF16 scan with final states S went token by token: then its states are bit for
+    bit those of the FP32 scan (which always does) of the same values. Chunks sum otherwise."""
+    wide = dataclasses.replace(case, io="f32")
+    x = [t.float() for t in ins]
+    return torch.equal(run(wide, x)[1], S)
+
+
+@pytest.mark.parametrize("P", [8, 40, 64, 128])
+@pytest.mark.parametrize("N", [16, 32, 64, 128])
+@pytest.mark.parametrize("lens", [(7,), (8, 8, 8), (9, 1, 0, 8, 17), (30, 29, 16, 15, 24, 25)], ids=str)
+def test_short_bf16_sequences_token_by_token(N, P, lens):
+    """Around the stages of 8 tokens and the batches of 4, with state rows that fill the blocks of
+    32 to 256 and that do not. Everything is FP32 until the outputs are rounded."""
+    case = Case("short", 4, 2, P, N, lens, "bf16", resume="some", rows=len(lens) + 2, seed=N + P, lead=1, tail=3)
+    ins = scan_inputs(case)
+    y, S, cu, seqs, resume = run(case, ins, max_len=max(lens))
+    assert token_by_token(case, ins, S)
+    want, mag = oracle(ins, cu, seqs, resume)
+    live = check(case, ins, y, S, want, mag, cu, seqs, resume)
+    by = (2 * max(lens) + N + 8) * U32 * mag[0] + HALF["bf16"] * np.abs(want[0]) + 1e-37  # no parts
+    assert_within(f64(y)[live], want[0][live], by[live], "y")
+    assert (y[torch.from_numpy(~live).cuda()] == 7).all()
+
+
+@pytest.mark.parametrize("N", [16, 64, 128])
+@pytest.mark.parametrize("length,serial", [(1, True), (29, True), (30, True), (31, False), (32, False)])
+def test_the_choice_of_kernel_by_the_longest_length(N, length, serial):
+    case = Case("side", 4, 2, 40, N, (length,) * 3, "bf16", resume="some", seed=length)
+    ins = scan_inputs(case)
+    y, S, cu, seqs, resume = run(case, ins, max_len=length)
+    check(case, ins, y, S, *oracle(ins, cu, seqs, resume), cu, seqs, resume)
+    assert token_by_token(case, ins, S) == serial
