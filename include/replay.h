@@ -357,15 +357,20 @@ int replay_verify_static_scratch(replay_ctx* ctx, int32_t n_pos, const void* q, 
  * decreasing; lengths of zero are allowed; tokens outside every sequence are neither read
  * nor written). Sequence s owns row seqs[s] of the state (device int32 [n_seqs], distinct;
  * NULL = row s, n_seqs <= batch). A negative id is padding: that sequence is skipped, its
- * outputs are left as they were. A sequence whose
- * bounds fall or lie outside the tokens is skipped and reported, and the others are served;
- * but where bounds fall, a token that two sequences then hold has unspecified outputs, and
- * replay_prompt_inputs, which searches the bounds, may pass over good sequences or tokens of
- * theirs. resume[s] != 0 (device uint8 [n_seqs]; NULL = none) continues sequence s from its
- * row; else it starts from zero. Rows that no sequence owns are left as they were. `status`
- * (device int32 [1], may be NULL) receives REPLAY_DEV_SEQS. No call allocates device memory or synchronises; each can be captured
- * into a CUDA graph (once one call of the same kind has run outside the capture), and
- * replayed on new contents of the same buffers, cu_seqlens, seqs and resume among them.
+ * outputs are left as they were. A sequence whose bounds fall or lie outside the tokens is
+ * skipped and reported, and the others are served; but where bounds fall, a token that two
+ * sequences then hold has unspecified outputs, and replay_prompt_inputs, which searches the
+ * bounds, may pass over good sequences or tokens of theirs. resume[s] != 0 (device uint8
+ * [n_seqs]; NULL = none) continues sequence s from its row; else it starts from zero. Rows
+ * that no sequence owns are left as they were.
+ *
+ * `status` (device int32 [1], may be NULL) receives REPLAY_DEV_SEQS, and, from the scan,
+ * REPLAY_DEV_WAIT_TIMEOUT; a block of the scan whose wait gave up also puts NaN over the
+ * outputs and final states that were its to make, so that nobody takes old ones for them.
+ *
+ * No call allocates device memory or synchronises; each can be captured into a CUDA graph
+ * (once one call of the same kind has run outside the capture), and replayed on new contents
+ * of the same buffers, cu_seqlens, seqs and resume among them.
  *
  * Row strides ldx, ldr, ldz are in elements, so that the caller may pass slices of its
  * projection's rows; x and z rows start on 16-byte boundaries. */

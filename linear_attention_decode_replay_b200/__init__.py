@@ -616,7 +616,8 @@ def prompt_scan(cfg: Config, S, q, k, v, dt, a, cu_seqlens, seqs=None, resume=No
     row seqs[s] of S [batch][H][P][N] (FP32) where resume[s], else from zero; the final
     states go back to S. q, k [T][G][N], v [T][H][P] (io), dt, a [T][H] (FP32), cu_seqlens
     int32 [n + 1], seqs int32 [n], resume uint8 [n]. max_len, if known, steers how the work
-    is split. Returns y [T][H][P] (io)."""
+    is split. Returns y [T][H][P] (io). A scan that fails on the device (its wait gave up,
+    DEV_WAIT_TIMEOUT in status) leaves NaN in place of what it could not make."""
     _n_seqs(cu_seqlens)
     dev, T = _device_of(q, "q"), q.shape[0]
     c = cfg._layer[0]

@@ -160,6 +160,73 @@ __device__ __forceinline__ bool find_segment(const Packed& pk, int seg_tokens, i
   return false;
 }
 
+__device__ __forceinline__ bool takes_longest_first(const ScanParams& p) {
+  return !p.seg_tokens && p.pk.n_seqs <= kSortSeqs;
+}
+
+// Unit number `id`, by a whole warp; false if there is nothing to do for it.
+template <bool LOCAL>
+__device__ __forceinline__ bool unit_of(const ScanTcParams& tp, TcBars* bars, int id, Unit& u) {
+  const ScanParams& p = tp.s;
+  const int ptiles = (p.P + kPT - 1) / kPT;
+  int s = id / (p.H * ptiles), seg = 0, segs = 1;
+  // the length of a segment is read where it is needed: a register of it would spill
+  if (p.seg_tokens && !find_segment(p.pk, *const_cast<volatile int*>(&bars->seg_tokens), s, s, seg, segs)) return false;
+  if (LOCAL && seg == segs - 1) return false;
+  if (takes_longest_first(p)) s = bars->order[s];
+  int64_t begin, end;
+  if (!seq_bounds(p.pk, s, begin, end)) return false;
+  if (segs > 1) {
+    begin += (int64_t)seg * p.seg_tokens;
+    if (seg < segs - 1) end = begin + p.seg_tokens;
+  }
+  u.row = seq_row(p.pk, s);
+  if (u.row < 0) return false;
+  u.begin = (int)begin, u.len = (int)(end - begin);
+  u.h = id / ptiles % p.H, u.g = u.h / (p.H / p.G), u.p0 = id % ptiles * kPT;
+  u.id = id;
+  u.from = LOCAL ? 0 : segs > 1 ? 2 : p.pk.resume && p.pk.resume[s] ? 1 : 0;
+  u.to = LOCAL ? 2 : seg == segs - 1 ? 1 : 0;
+  return true;
+}
+
+// A block's unit of a round. After the first round the blocks take units in turned order: long
+// ones go with short ones.
+__device__ __forceinline__ int id_of(int round) {
+  return round * gridDim.x + (round == 0 ? blockIdx.x : gridDim.x - 1 - blockIdx.x);
+}
+
+// After a wait that gave up: NaN over the outputs and states that the block was to make, by
+// warps 0 to 7, so that the failure shows where the caller looks at no status word.
+template <bool LOCAL>
+__device__ __forceinline__ void spoil(const ScanTcParams& tp, TcBars* bars) {
+  const ScanParams& p = tp.s;
+  const int lane = threadIdx.x & 31;
+  const float nan = __uint_as_float(0x7FC00000u);
+#pragma unroll 1
+  for (int round = threadIdx.x / 32; round * (int64_t)gridDim.x < tp.units; round += kWarpU) {
+    const int id = id_of(round);
+    Unit u;
+    if (id >= tp.units || !unit_of<LOCAL>(tp, bars, id, u)) continue;
+    const int rows = p.P - u.p0 < kPT ? p.P - u.p0 : kPT;
+    float* state = LOCAL ? p.seg_state + (size_t)id * kPT * p.N : p.S + (((size_t)u.row * p.H + u.h) * p.P + u.p0) * p.N;
+    if (u.to)
+#pragma unroll 1
+      for (int i = lane; i < rows * p.N; i += 32) state[i] = nan;
+    if (LOCAL) {
+      if (lane == 0) p.seg_decay[id] = nan;
+      continue;
+    }
+    const int vecs = rows / 8;  // P is a multiple of 8
+#pragma unroll 1
+    for (int64_t i = lane; i < (int64_t)u.len * vecs; i += 32) {
+      const int64_t t = u.begin + i / vecs;
+      uint16_t* y = static_cast<uint16_t*>(p.y) + ((size_t)t * p.H + u.h) * p.P + u.p0 + i % vecs * 8;
+      *reinterpret_cast<uint4*>(y) = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+    }
+  }
+}
+
 // LOCAL: only the segments' own states, from zero, for those with a segment behind them.
 template <int NT, bool LOCAL>
 __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_constant__ ScanTcParams tp) {
@@ -204,7 +271,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
   tc_fence_after();
   const uint32_t tmem = uniform(bars->tmem);
   volatile uint32_t* abort = &bars->abort;
-  volatile int* seg_tokens = &bars->seg_tokens;
 
   // waits for a phase; false if it takes too long (the block then winds down: every other
   // wait of its ends within the same time)
@@ -252,9 +318,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
     regs_down<kRegsCopy>();
     // ------------------------------------------------------------ plan
     if (warp == kWarpPlan) {
-      const int ptiles = (p.P + kPT - 1) / kPT, heads = p.H * ptiles;
-      const bool sorted = !p.seg_tokens && p.pk.n_seqs <= kSortSeqs;
-      if (sorted) {
+      if (takes_longest_first(p)) {
         for (int s = lane; s < p.pk.n_seqs; s += 32) {
           const int len = p.pk.cu[s + 1] - p.pk.cu[s];
           int rank = 0;
@@ -270,30 +334,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
       bool more = true;
 #pragma unroll 1
       for (int round = 0; more; ++round) {
-        // after the first round the blocks take units in turned order: long ones go with short ones
-        const int id = round * gridDim.x + (round == 0 ? blockIdx.x : gridDim.x - 1 - blockIdx.x);
+        const int id = id_of(round);
         Unit u;
         u.len = -1;
         more = round * (int64_t)gridDim.x < tp.units;
         if (more) {
-          if (id >= tp.units) continue;
-          int s = id / heads, seg = 0, segs = 1;
-          if (p.seg_tokens && !find_segment(p.pk, *seg_tokens, s, s, seg, segs)) continue;
-          if (LOCAL && seg == segs - 1) continue;
-          if (sorted) s = bars->order[s];
-          int64_t begin, end;
-          if (!seq_bounds(p.pk, s, begin, end)) continue;
-          if (segs > 1) {
-            begin += (int64_t)seg * p.seg_tokens;
-            if (seg < segs - 1) end = begin + p.seg_tokens;
-          }
-          u.row = seq_row(p.pk, s);
-          if (u.row < 0) continue;
-          u.begin = (int)begin, u.len = (int)(end - begin);
-          u.h = id / ptiles % p.H, u.g = u.h / (p.H / p.G), u.p0 = id % ptiles * kPT;
-          u.id = id;
-          u.from = LOCAL ? 0 : segs > 1 ? 2 : p.pk.resume && p.pk.resume[s] ? 1 : 0;
-          u.to = LOCAL ? 2 : seg == segs - 1 ? 1 : 0;
+          if (id >= tp.units || !unit_of<LOCAL>(tp, bars, id, u)) continue;
           if (u.from && lane == 0)  // the state that it starts from into L2
             prefetch_l2(u.from == 2 ? p.seg_state + (size_t)id * kPT * p.N
                                     : p.S + (((size_t)u.row * p.H + u.h) * p.P + u.p0) * p.N,
@@ -772,8 +818,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (*abort && p.pk.status && threadIdx.x == 0) atomicOr(p.pk.status, kErrWaitTimeout);
   if (warp == kWarpTma) tmem_free(tmem, 512);
+  if (*abort && threadIdx.x < 32 * kWarpU) {  // the warps that kept the registers of the launch
+    if (p.pk.status && threadIdx.x == 0) atomicOr(p.pk.status, kErrWaitTimeout);
+    spoil<LOCAL>(tp, bars);
+  }
 }
 
 constexpr int kCarryAhead = 8;  // segments whose loads are in flight together
