@@ -43,20 +43,21 @@ FALLBACK_HBM_GBS = 6650.0
 # DRAM traffic of one replay_step launch (flush and output-only launches averaged over a
 # window) of the workload it was captured on, from an ncu capture, and the hash of the
 # kernel sources it applies to. For another workload, or once the sources change, the
-# figure does not apply and is reported as null. The hash covers the decode kernels' sources.
-# "captured_on" is that of every source at the capture itself (the decode kernels' differ
-# from the current ones only in the kernel's header comment and in two unused device helpers
-# since removed). Measured on the fold launch
-# and an 8-entry output-only launch: (fold + 15 x output-only) / 16.
+# figure does not apply and is reported as null. The hash covers the sources of the decode
+# kernels and of their launches. "captured_on" is that of every source at the capture itself
+# (those differ from the current ones only in the kernel's header comment, in two unused
+# device helpers since removed, and in that replay_ctx.h was part of replay_api.cu).
+# Measured on the fold launch and an 8-entry output-only launch: (fold + 15 x output-only) / 16.
 NCU_TRAFFIC = {"workload": "mamba2_b256",
-               "sources_sha256": "8b1a1e36f94d6b68f313ab777865c1610482210ba78a3f2ab8c64abc701e13ed",
+               "sources_sha256": "9607201e345fac8874c4a7f158303486798e6c2a16533b8378434ace60461588",
                "captured_on": "e21d8dddf37eccd0f0edeb00f8e98d6b152826fcde7bec1dd8fcedccd8204fe7",
                "bytes_per_launch": 646.1e6}
 
 
-DECODE_SOURCES = ("replay_device.cuh", "replay_instances.cuh", "replay_kernel.cuh", "replay_kernels_n128.cu",
-                  "replay_kernels_n16.cu", "replay_kernels_n32.cu", "replay_kernels_n64.cu", "replay_kparams.h",
-                  "replay_launch.h", "replay_small.cu")
+# the decode kernels and what lays out and makes their launches
+DECODE_SOURCES = ("replay_api.cu", "replay_ctx.h", "replay_device.cuh", "replay_instances.cuh", "replay_kernel.cuh",
+                  "replay_kernels_n128.cu", "replay_kernels_n16.cu", "replay_kernels_n32.cu", "replay_kernels_n64.cu",
+                  "replay_kparams.h", "replay_launch.h", "replay_small.cu")
 
 
 def kernel_sources_hash() -> str:
