@@ -220,8 +220,9 @@ int replay_rollback(replay_ctx* ctx, const int32_t* n_keep, replay_stream_t stre
 int replay_flush(replay_ctx* ctx, const uint8_t* mask, replay_stream_t stream);
 
 /* ---- Snapshots of single sequences (export / import) ----
- * A sequence's decode state is its checkpoint, its committed buffer entries and their
- * count, nothing else (blog "Decodificacion estandar"; abstract: the buffer keeps the
+ * A sequence's decode state in a context is its checkpoint, its committed buffer entries and
+ * their count, nothing else (what a layer keeps beside the recurrence, as the rows of `conv`
+ * that replay_prompt_inputs and its like update, is the caller's to copy along) (blog "Decodificacion estandar"; abstract: the buffer keeps the
  * raw inputs since the checkpoint). A snapshot holds exactly that, as one self-describing
  * block per sequence: a prefix-cache or migration unit (the hamidun.com page and the video
  * takeaways on snapshots and prefix caching). Layout of one block, replay_snapshot_bytes
@@ -386,7 +387,11 @@ int replay_verify_static_scratch(replay_ctx* ctx, int32_t n_pos, const void* q, 
  *   x:    device [tokens] rows of D io, ldx apart     raw: [tokens] rows of H io, ldr apart
  *   w:    device [width][D] FP32, width 2..4 (w[width - 1] takes the token itself)
  *   bias: [D] FP32 or NULL (w and bias 16-byte aligned)   dt_bias: [H] FP32 or NULL   A: [H] FP32
- *   conv: device [batch][width - 1][D] io, oldest row first (updated)
+ *   conv: device [batch][width - 1][D] io, oldest row first (updated). It is the caller's:
+ *         replay_rollback, replay_export and replay_import know nothing of it. For a verify
+ *         round of which only some positions may be kept, copy the rows first; after the
+ *         rollback, put them back and call again over the kept tokens alone (each
+ *         sequence's others as a padding sequence, id -1, behind them)
  *   q, k: device [tokens][G][N] io   v: [tokens][H][P] io   dt, a: [tokens][H] FP32 (written)
  * No output may overlap x, raw or conv. */
 int replay_prompt_inputs(const replay_config* cfg, int32_t width, int64_t tokens, const void* x, int64_t ldx,

@@ -418,3 +418,45 @@ def test_a_prefill_that_skips_a_sequence_leaves_its_row(bounds, ids):
     assert first.read_counts() == [2 if b == row else 0 for b in range(3)]
     assert torch.equal(first.buffers["S0"][row], plain.buffers["S0"][row])
     assert torch.equal(first.step(*token)[row], plain.step(*token)[row])
+
+
+def test_the_inputs_of_a_verify_round_that_keeps_some_positions():
+    """The rollback knows nothing of the convolution's state: put back, and brought forward by the
+    kept positions alone, it is what those tokens leave one by one, and decoding goes on as if
+    the others had never been."""
+    H, G, P, N, B, n = 4, 2, 24, 32, 4, 5
+    keep = [0, 2, 5, 1]
+    cfg = lar.Config(batch=B, heads=H, groups=G, P=P, N=N, L=8, max_pos=n, io="f32")
+    case = Case("verify", H, G, P, N, (n,) * B, "f32", rows=B)
+    r = layer_rows(case)
+    x, raw, w, A, conv = r["x"], r["raw"], r["w"], r["A"], r["conv"].clone()
+    layer = lar.Replay(cfg, lar.alloc_buffers(cfg, "cuda"))
+    S0 = 0.1 * torch.randn(B, H, P, N, device="cuda")
+    layer.buffers["S0"].copy_(S0)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    on = torch.ones(2 * B, dtype=torch.uint8, device="cuda")
+    before = conv.clone()
+    ins = lar.prompt_inputs(cfg, conv, x, raw, w, A, i32([n * b for b in range(B + 1)]), resume=on[:B])
+    layer.verify(*(t.unflatten(0, (B, n)) for t in ins))
+    layer.rollback(i32(keep))
+    moved = conv.clone()
+    conv.copy_(before)
+    cu = [0]
+    for b in range(B):
+        cu += [n * b + keep[b], n * (b + 1)]
+    lar.prompt_inputs(cfg, conv, x, raw, w, A, i32(cu), seqs=i32([s for b in range(B) for s in (b, -1)]), resume=on)
+    # the same tokens one by one, each sequence in a layer of its own
+    one = lar.Config(batch=1, heads=H, groups=G, P=P, N=N, L=8, io="f32")
+    last = layer_rows(Case("last", H, G, P, N, (1,) * B, "f32", seed=8))
+    want = []
+    for b in range(B):
+        c, single = r["conv"][b:b + 1].clone(), lar.Replay(one, lar.alloc_buffers(one, "cuda"))
+        single.buffers["S0"].copy_(S0[b:b + 1])
+        for t in range(keep[b]):
+            single.step_resident(single.append_inputs(c, x[n * b + t][None], raw[n * b + t][None], w, A)[0])
+        assert torch.equal(conv[b], c[0])
+        assert torch.equal(moved[b], c[0]) == (keep[b] == n)
+        want.append(single.step_resident(single.append_inputs(c, last["x"][b:b + 1], last["raw"][b:b + 1], w, A)[0]))
+    y = layer.step_resident(layer.append_inputs(conv, last["x"], last["raw"], w, A)[0])
+    assert ro.relative_error(f64(y), f64(torch.cat(want))) <= 1e-5  # FP32, the same entries in other launches
+    assert layer.read_counts() == [k + 1 for k in keep] and layer.check_status() == 0
