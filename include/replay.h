@@ -428,6 +428,14 @@ int64_t replay_prompt_scan_scratch(const replay_config* cfg, int64_t tokens, int
 /* The selective scan of packed prompts: per sequence and head, token by token,
  *   S <- a_t S + Delta_t v_t k_t^T,   y_t = S q_t   (head h uses k and q of group h / (H/G)),
  * from row seqs[s] of S (resume) or zero, whose final state is written back there.
+ * Sums, states and decays are FP32. FP32 inputs and short BF16 sequences go token by token,
+ * longer BF16 sequences in chunks on the tensor cores. There the factors C = (q_i . k_j) decay
+ * Delta and S of the outputs are sums of two BF16 parts, each within 2^-16 of itself: of an
+ * output's terms' magnitudes 2^-14 at most, below the half step of 2^-8 of BF16 outputs unless
+ * their terms cancel. (The update of S takes three parts, 2^-23.) A caller that needs more
+ * passes FP32 inputs. In a chunk q_i . k_j and the products of consecutive decays must be
+ * within FP32's range: |a| <= 1, which Delta and A that are not negative give, cannot leave it
+ * upwards (a product below it is zero), nor can larger ones whose products stay under 2^127.
  *   q, k: device [tokens][G][N] io   v: [tokens][H][P] io   dt, a: [tokens][H] FP32
  *   S: device [batch][H][P][N] FP32 (updated)   y: device [tokens][H][P] io (written)
  *   scratch: device, replay_prompt_scan_scratch bytes, 256-byte aligned (NULL if 0); its
@@ -447,8 +455,8 @@ int64_t replay_prefill_scratch(const replay_ctx* ctx, int64_t tokens, int32_t n_
  * folded into its checkpoint first. Afterwards the served sequences' buffers are empty,
  * their checkpoints hold the prompts' final states and a read copy is refreshed; the
  * others are as they were. Arguments as replay_prompt_scan. Counts as one replay_flush
- * towards the even number of calls in a captured graph where resume is given, and as no
- * call where it is NULL. Returns REPLAY_EPENDING while a verify awaits its rollback. */
+ * towards the even number of calls in a captured graph where resume is given and n_seqs is
+ * not 0, and as no call otherwise. Returns REPLAY_EPENDING while a verify awaits its rollback. */
 int replay_prefill(replay_ctx* ctx, int64_t tokens, const void* q, const void* k, const void* v, const float* dt,
                    const float* a, const int32_t* cu_seqlens, const int32_t* seqs, const uint8_t* resume,
                    int32_t n_seqs, int64_t max_len, void* y, void* scratch, int64_t scratch_bytes,

@@ -11,7 +11,7 @@
 // state keeps FP32 accuracy), S and P in two (2^-16, under the outputs' own rounding of 2^-8).
 // dS is summed apart from S, since the accumulators do not round to nearest and S may hold
 // thousands of tokens. Decays are products, never exponentials of differences: a = 0 and any
-// sign are exact. A few long sequences are cut into segments: the segments' own states first
+// sign need no care, and magnitudes above 1 only that no run of them overflows. A few long sequences are cut into segments: the segments' own states first
 // (LOCAL: k and v only), then the states that they start from, then all segments at once.
 //
 // What bounds it: a chunk of one head at N = 128 takes an SM about 4900 cycles. Its products

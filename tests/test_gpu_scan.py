@@ -336,3 +336,45 @@ def test_the_choice_of_kernel_by_the_longest_length(N, length, serial):
     y, S, cu, seqs, resume = run(case, ins, max_len=length)
     check(case, ins, y, S, *oracle(ins, cu, seqs, resume), cu, seqs, resume)
     assert token_by_token(case, ins, S) == serial
+
+
+@pytest.mark.parametrize("lens,decay", [((300, 20), 1.2), ((300, 20), -1.1), ((100, 120), 2.0), ((128, 129), 1.9),
+                                        ((3000,), 1.01), ((3000, 17), -1.02)])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_scan_with_decays_above_one(io, lens, decay):
+    """States that grow, up to 2^124 of what came in: the products of a chunk's and a segment's
+    decays stay inside FP32's range, and the bounds are those of any decay."""
+    case = Case("grow", 2, 1, 64, 128, lens, io, resume="all")
+    ins = scan_inputs(case, decay=decay)
+    y, S, cu, seqs, resume = run(case, ins)
+    check(case, ins, y, S, *oracle(ins, cu, seqs, resume), cu, seqs, resume)
+
+
+def test_scan_with_decays_on_both_sides_of_one():
+    case = Case("both", 4, 2, 40, 64, (2900, 300), "bf16", resume="some", rows=3)
+    ins = scan_inputs(case)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    ins[4] = 0.6 + 0.7 * torch.rand(ins[4].shape, generator=g, device="cuda")
+    y, S, cu, seqs, resume = run(case, ins)
+    check(case, ins, y, S, *oracle(ins, cu, seqs, resume), cu, seqs, resume)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("what", ["q", "k", "v", "dt", "a"])
+@pytest.mark.parametrize("at", [0, 1000, 4000, 5002])
+def test_bad_values_in_a_sequence_of_segments(bad, what, at):
+    """As in a short sequence: the tokens before, the other sequence and the other head stay as
+    they were, and the same outputs and state elements are finite as in the definition."""
+    case = Case("bad_long", 2, 2, 64, 128, (5003, 40), "bf16", resume="all", seed=3)
+    ins = scan_inputs(case)
+    y0, S0, cu, seqs, resume = run(case, ins)
+    x = [t.clone() for t in ins]
+    x["q k v dt a".split().index(what)][(at, 0, 5) if what in "qkv" else (at, 0)] = bad
+    y1, S1, *_ = run(case, x)
+    same = torch.ones(case.T, case.H, dtype=torch.bool, device="cuda")
+    same[at:5003, 0] = False
+    assert torch.equal(y0[same], y1[same])
+    assert torch.equal(S0[1], S1[1]) and torch.equal(S0[0, 1], S1[0, 1])
+    want, wS = lo.prompt_scan(*[f64(i) for i in x], f64(cu), f64(seqs), f64(resume))
+    assert np.array_equal(np.isfinite(f64(y1)), np.isfinite(want))
+    assert np.array_equal(np.isfinite(f64(S1)), np.isfinite(wS))
