@@ -21,6 +21,8 @@
 // the 64-head layer (G = 64): 104 us, 63 % of the measured copy bandwidth; 32768 tokens of one
 // sequence (G = 8): 530 us, of which 165 us the segments' own states. One part each for P
 // and S gained 3 to 5 % and raised the outputs' error from 1.7e-3 to 2.3e-3: left at two.
+#include <atomic>
+
 #include "layer_device.cuh"
 #include "tcgen05.cuh"
 
@@ -910,7 +912,7 @@ bool tile_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int w
 template <int NT, bool LOCAL>
 cudaError_t launch_tc(ScanTcParams& tp, int64_t units, int num_sms, cudaStream_t s) {
   constexpr int smem = TcLayout<NT, LOCAL>::bytes;
-  static bool configured[64] = {false};  // per device; setting it twice does no harm
+  static std::atomic<bool> configured[64];  // per device; two threads may both set the attribute, to the same
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
