@@ -233,14 +233,21 @@ def _device_of(t, name):
     return t.get_device()
 
 
+# The current device and a device's current stream, by torch's short forms, or, where a torch
+# has none, by its public calls.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _on(dev, stream, body):
     """body(raw stream) with device `dev` current and `stream` (None: its current one) the
     stream of the allocations in it, so that none is handed to another stream's work early."""
-    if stream is None and torch._C._cuda_getDevice() == dev:
-        return body(torch._C._cuda_getCurrentRawStream(dev))
+    if stream is None and _current_device() == dev:
+        return body(_raw_stream(dev))
     with torch.cuda.device(dev):
         if stream is None:
-            return body(torch._C._cuda_getCurrentRawStream(dev))
+            return body(_raw_stream(dev))
         with torch.cuda.stream(stream):
             return body(stream.cuda_stream)
 

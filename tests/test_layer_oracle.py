@@ -231,3 +231,17 @@ def test_a_config_that_was_used_is_copied_like_a_new_one(again):
     assert other == cfg and hash(other) == hash(cfg) and vars(cfg) == fields == vars(other)
     with pytest.raises(ValueError, match="CUDA"):
         lar.gated_norm(other, torch.zeros(3, 4, 16), torch.zeros(3, 64).bfloat16(), torch.zeros(64))
+
+
+def test_the_binding_needs_no_private_call_of_torch(monkeypatch):
+    """Loaded with a torch that lacks its short forms, it takes the public calls."""
+    import importlib.util
+
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    spec = importlib.util.find_spec(lar.__name__)
+    other = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(other)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev: type("S", (), {"cuda_stream": 40 + dev}))
+    monkeypatch.setattr(other, "_current_device", lambda: 3)
+    assert other._on(3, None, lambda raw: raw) == 43
