@@ -380,7 +380,8 @@ int replay_verify_static_scratch(replay_ctx* ctx, int32_t n_pos, const void* q, 
  * channels a row, v (H*P), then k (G*N), then q (G*N). Per channel and token, within the
  * sequence,
  *   c_t = bias + sum_{i < width} w[i] x[t - (width - 1) + i],   out = c_t sigmoid(c_t),
- * where the rows before the first token are the state's (resume) or zero. Per head
+ * where the rows before the first token are the state's (resume) or zero (the sigmoid of BF16
+ * outputs is within 2^-19 of itself for |c_t| < 16; outputs under 2^-119 may be 0). Per head
  *   Delta = softplus(raw + dt_bias),   a = exp(-Delta A).
  * The state's row becomes the last width - 1 rows of x (with the old rows before them
  * where the sequence is shorter).

@@ -89,12 +89,12 @@ int check_scratch(const void* scratch, int64_t have, int64_t need) {
   return aligned(scratch, 256) ? REPLAY_OK : REPLAY_EALIGN;
 }
 
-// The scratch of one scan: the segments' states, then their decays.
 // The serial kernel takes FP32 inputs, and BF16 sequences of few tokens, where the tensor
 // cores' chunks of 128 are mostly empty: a chunk of one head takes an SM about 6 us with its
-// state, a token of the serial kernel 0.27 us in each of a few blocks an SM (256 sequences of
-// the 64-head layer: 16 tokens each 380 against 672 us, 24 tokens 526 against 668 us, 32 tokens 689 against
-// 673 us).
+// state, a token of the serial kernel 0.27 us in each of a few blocks an SM. 256 sequences of
+// the 64-head layer of 64 x 128: 16 tokens each 380 against 672 us, 24 tokens 526 against 668,
+// 32 tokens 689 against 673; of 32 heads of 128 x 128 the same within 3 %. The rule is N = 128's:
+// at N = 64 (8 heads of 64 x 64) the serial kernel still leads at 40 tokens, 58 against 90 us.
 bool on_tensor_cores(const replay_config& c, int64_t tokens, int32_t n_seqs, int64_t max_len) {
   if (c.io != REPLAY_BF16 || tokens == 0) return false;
   constexpr int64_t kFew = 30;
@@ -106,6 +106,7 @@ bool on_tensor_cores(const replay_config& c, int64_t tokens, int32_t n_seqs, int
 int64_t segment_units(const replay_config& c, const replay::ScanSplit& sp) {
   return (int64_t)sp.max_segs * c.heads * ((c.P + 63) / 64);
 }
+// The scratch of one scan: the segments' states, then their decays.
 int64_t scan_scratch(const replay_config& c, int64_t tokens, int32_t n_seqs, int64_t max_len) {
   if (!on_tensor_cores(c, tokens, n_seqs, max_len)) return 0;
   const replay::ScanSplit sp = replay::scan_split(tokens, n_seqs, max_len, c.heads, c.P);

@@ -90,9 +90,11 @@ struct Vec<__nv_bfloat16, 4> {
   }
   __device__ __forceinline__ static uint2 zero() { return make_uint2(0u, 0u); }
 };
-// x sigmoid(x). For BF16 results the hardware's exponential and reciprocal, each within a
-// few units of 2^-23 (the result's own rounding is 2^-9); for FP32 results the accurate
-// exponential and a division within 2 steps (results under 2^-120 may become 0).
+// x sigmoid(x). For BF16 results the hardware's exponential and reciprocal: each is within a
+// few units of 2^-23, and x log2(e), rounded before the exponential, adds |x| 2^-24 (so that
+// the result is within 2^-19 for |x| < 16, and its own rounding is 2^-8); results under 2^-119
+// may become 0. For FP32 results the accurate exponential and a division within 2 steps
+// (results under 2^-119 may become 0).
 template <typename IO>
 __device__ __forceinline__ float silu(float x) {
   if constexpr (sizeof(IO) == 2) {

@@ -17,10 +17,13 @@
 // What bounds it: a chunk of one head at N = 128 takes an SM about 4900 cycles. Its products
 // are 2300 of them (tensor pipe 46 % active), its wavefronts in the shared-memory pipe 2900, its
 // instructions 2600 a scheduler; the chain C - P - Y1 within a chunk, whose P lies where the
-// next C will (tensor memory is full), keeps them from overlapping further. 8192 tokens of
-// the 64-head layer (G = 64): 104 us, 63 % of the measured copy bandwidth; 32768 tokens of one
-// sequence (G = 8): 530 us, of which 165 us the segments' own states. One part each for P
-// and S gained 3 to 5 % and raised the outputs' error from 1.7e-3 to 2.3e-3: left at two.
+// next C will, keeps them from overlapping further. (The parts of Y2 and dS lie side by side
+// and fill tensor memory. Summed onto one another, S's second part and U's third would free the
+// 128 columns of a second C, for narrower products; not tried.) 8192 tokens of the 64-head layer
+// (G = 64): 104 us, 63 % of the measured copy bandwidth; 32768 tokens of one sequence (G = 8):
+// 500 us, of which a third the segments' own states. Both at 1965 MHz: run for a second on end they
+// meet the power limit, and at 1575 and 1650 MHz take 127 and 587 us. One part each for P and
+// S gained 3 to 5 % and raised the outputs' error from 1.7e-3 to 2.3e-3: left at two.
 #include <atomic>
 
 #include "layer_device.cuh"
