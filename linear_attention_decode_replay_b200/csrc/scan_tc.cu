@@ -360,26 +360,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) scan_tc_kernel(const __grid_con
     }
     // ------------------------------------------------------------ TMA
     if (warp == kWarpTma && lane == 0) {
-      // q of a chunk, then k and v of the next: the order in which their tiles fall free
+      // q of a chunk, then k and v of the next: the order in which their tiles fall free. The q
+      // first, and then the look for the next chunk: behind units without any it comes only once
+      // every role has gone on to them.
       int n = 0, nq = 0;  // tiles of k and v, and of q, issued
       Unit u;
       int chunks = 0, c = 0, tq = -1, gq = 0;  // the chunk whose q is due: its first token and group
 #pragma unroll 1
       for (int k = 0; chunks >= 0;) {
-        while (chunks >= 0 && c >= chunks) chunks = take_unit(u, k++), c = 0;
-        const int t = u.begin + c * kChunk;
         if (!LOCAL && tq >= 0) {
           if (nq >= 1 && !wait(&bars->q_empty, nq - 1)) break;
           mbar_arrive_expect_tx(&bars->q_full, Lay::kQK);
 #pragma unroll 1
-          for (int i = 0; i < NT / 64; ++i) {
-            tma_load3(smem + Lay::q + i * kTile, &tp.q, 64 * i, gq, tq, &bars->q_full);
-            // q has one tile, so its next load starts late: from L2
-            if (chunks >= 0) tma_prefetch3(&tp.q, 64 * i, u.g, t);
-          }
+          for (int i = 0; i < NT / 64; ++i) tma_load3(smem + Lay::q + i * kTile, &tp.q, 64 * i, gq, tq, &bars->q_full);
           ++nq;
         }
+        while (chunks >= 0 && c >= chunks) chunks = take_unit(u, k++), c = 0;
         if (chunks < 0) break;
+        const int t = u.begin + c * kChunk;
+        if (!LOCAL && tq >= 0) {  // q has one tile, so its next load starts late: from L2
+#pragma unroll 1
+          for (int i = 0; i < NT / 64; ++i) tma_prefetch3(&tp.q, 64 * i, u.g, t);
+        }
         const int b = n & 1;
         if (n >= 2 && !wait(&bars->k_empty[b], (n >> 1) - 1)) break;
         mbar_arrive_expect_tx(&bars->k_full[b], Lay::kQK);

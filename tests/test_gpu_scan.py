@@ -378,3 +378,21 @@ def test_bad_values_in_a_sequence_of_segments(bad, what, at):
     want, wS = lo.prompt_scan(*[f64(i) for i in x], f64(cu), f64(seqs), f64(resume))
     assert np.array_equal(np.isfinite(f64(y1)), np.isfinite(want))
     assert np.array_equal(np.isfinite(f64(S1)), np.isfinite(wS))
+
+
+@pytest.mark.parametrize("case", [
+    Case("one_of_many", 16, 4, 64, 128, (300,) + (0,) * 63, "bf16", resume="some", rows=64),
+    Case("every_fifth", 16, 4, 64, 128, tuple(0 if i % 5 else 50 + i for i in range(100)), "bf16", resume="some", rows=101),
+    Case("every_third", 16, 2, 128, 64, tuple(0 if i % 3 else 150 for i in range(48)), "bf16", resume="all", rows=48),
+    Case("few_tokens", 6, 2, 256, 16, (3, 3, 1, 5, 0, 17, 0, 0, 2, 0, 2, 0, 1, 56, 1, 2, 6, 11, 0, 2, 1, 2, 8, 0, 1), "bf16",
+         resume="some", lead=26),
+    Case("long_and_empty", 2, 1, 64, 128, (3000,) + (0,) * 40, "bf16", resume="some", rows=41),
+], ids=lambda c: c.name)
+def test_many_sequences_without_tokens(case):
+    """A batch's empty places: a block takes several units without a chunk one after another, and
+    goes on; empty sequences keep their rows or make them zero."""
+    ins = scan_inputs(case)
+    y, S, cu, seqs, resume = run(case, ins)
+    check(case, ins, y, S, *oracle(ins, cu, seqs, resume), cu, seqs, resume)
+    again, S2, *_ = run(case, ins, max_len=max(case.lens))
+    check(case, ins, again, S2, *oracle(ins, cu, seqs, resume), cu, seqs, resume)
