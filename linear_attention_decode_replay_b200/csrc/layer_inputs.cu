@@ -5,8 +5,8 @@
 // One pass: every channel is read once and written once, so memory bandwidth bounds both
 // kernels; the exponential and the reciprocal of each output keep the special function
 // unit 61 % busy. Sums are FP32; q, k and v are rounded once, to the
-// layer's io type. 8192 tokens of 20480 BF16 channels: 135 us, 77 % of the measured copy
-// bandwidth; one token of 256 such rows: 18 us, 72 %.
+// layer's io type. 8192 tokens of 20480 BF16 channels: 137 us, 77 % of the measured copy
+// bandwidth; one token of 256 such rows: 18 us, 74 %.
 #include "layer_device.cuh"
 
 namespace replay {

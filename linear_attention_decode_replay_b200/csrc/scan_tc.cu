@@ -20,9 +20,9 @@
 // next C will, keeps them from overlapping further. (The parts of Y2 and dS lie side by side
 // and fill tensor memory. Summed onto one another, S's second part and U's third would free the
 // 128 columns of a second C, for narrower products; not tried.) 8192 tokens of the 64-head layer
-// (G = 64): 110 us, 59 % of the measured copy bandwidth; 32768 tokens of one sequence (G = 8):
-// 510 us, of which a third the segments' own states. Both at 1965 MHz: run for a second on end they
-// meet the power limit, and at 1600 and 1665 MHz take 126 and 580 us. One part each for P and
+// (G = 64): 109 us, 60 % of the measured copy bandwidth; 32768 tokens of one sequence (G = 8):
+// 511 us, of which a third the segments' own states. Both at 1965 MHz: run for a second on end they
+// meet the power limit, and at 1590 and 1657 MHz take 126 and 582 us. One part each for P and
 // S gained 3 to 5 % and raised the outputs' error from 1.7e-3 to 2.3e-3: left at two.
 #include <atomic>
 
